@@ -3,7 +3,9 @@
  * linear that consumes it (decode and prefill), the W4A8 decode over the
  * same stored weights, AWQ alpha/shrink candidate scoring and the
  * per-output-channel clipping search, the block-level (look-ahead) candidate
- * loss and search, as hand-written CUDA kernels for B200 (sm_100a).
+ * loss and search, the microscaled 4-bit floating-point quantization and
+ * linear, appending to and attention over an 8-bit paged KV cache, as
+ * hand-written CUDA kernels for B200 (sm_100a).
  *
  * Sources (model-card pages, cited by title and section):
  *   [rebuttal] "ghostchoir/rebuttal_w4g128_awq_w2": 'Model Details' table
@@ -72,7 +74,9 @@ typedef enum {
   W4_ERR_UNSUPPORTED = 4,    /* group != 128, grid larger than supported, ... */
   W4_ERR_WORKSPACE = 5,      /* workspace missing or smaller than required */
   W4_ERR_CUDA = 6,           /* a CUDA runtime call failed (launch, attribute, ...) */
-  W4_ERR_DEVICE_TIMEOUT = 7  /* a kernel gave up on a bounded wait (w4_device_error) */
+  W4_ERR_DEVICE_TIMEOUT = 7, /* a kernel gave up on a bounded wait (w4_device_error) */
+  W4_ERR_DEVICE_INDEX = 8    /* a kernel met an index outside the caller's buffers
+                                (w4_device_error) */
 } w4_status;
 
 /* Static, NUL-terminated description of a status code. */
@@ -583,12 +587,160 @@ w4_status w4_quantize_pack_rows(const void* w_bf16, int64_t N, int64_t K, int gr
                                 void* stream);
 
 /*
+ * Microscaled 4-bit floating point: e2m1 codes (magnitudes 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6) with a scale for each block of consecutive input channels.
+ *
+ *   W4_FP4_MX  blocks of 32; scale 2^e as the byte e + 127 (e8m0),
+ *              e = clamp(floor(log2 amax) - 2, -127, 127), -127 for a block
+ *              of zeros.
+ *   W4_FP4_NV  blocks of 16; scale an e4m3 byte s, in units of a float32
+ *              scale of the row (a row's value is code * s * row_scale).
+ *              Quantizing takes for the row the least power of two, at least
+ *              2^-126, with max|row| <= 6 * 448 * row_scale (1 for a row of
+ *              zeros) and s = e4m3(amax / (6 row_scale)); the linear takes
+ *              any row scales (for instance one tensor scale, repeated).
+ *   code = e2m1(x / scale), ties to even, saturating at 6, sign kept; 0 where
+ *   the block's scale is 0.  Every rounding is decided on exact values.
+ *
+ * Layout: codes uint8 [rows, K/2], channel 2i in the low and 2i + 1 in the
+ * high nibble of byte i.  Scale bytes in tiles of 128 rows x 4 blocks, tiles
+ * [ceil(rows/128)][blocks per row / 4] of 512 bytes; (row, block) is byte
+ * (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4 of its tile.  Bytes of
+ * rows behind the last are neither written nor used.
+ */
+#define W4_FP4_MX 0
+#define W4_FP4_NV 1
+
+/* Bytes of the scale tiles of a [R, K] matrix; 0 for sizes or a format that
+ * w4_fp4_quantize refuses. */
+size_t w4_fp4_scale_bytes(int64_t R, int64_t K, int format);
+
+/*
+ * w4_fp4_quantize -- quantizes a bf16 matrix (a weight, or the activations of
+ * one linear call) to microscaled 4-bit floating point.
+ *
+ * x_bf16     device bf16 [R, K], rows ldx elements apart (ldx >= K, a
+ *            multiple of 8).  1 <= R <= 2^31-1, K a positive multiple of 128.
+ * codes_out  device uint8 [R, K/2] out.
+ * scales_out device, w4_fp4_scale_bytes(R, K, format) bytes out.
+ * row_scale_out  device float32 [R] out; NULL iff W4_FP4_MX.
+ * values_bf16  device bf16 [R, K] out: the values that the codes stand for
+ *            (exact in bf16 from 2^-126 up, rounded to its spacing of 2^-133
+ *            below), or NULL.
+ * Errors: W4_ERR_INVALID_ARG, W4_ERR_SHAPE, W4_ERR_ALIGNMENT (pointers 16
+ * bytes), W4_ERR_UNSUPPORTED (format).
+ */
+w4_status w4_fp4_quantize(const void* x_bf16, int64_t R, int64_t K, int64_t ldx, int format,
+                          uint8_t* codes_out, uint8_t* scales_out, float* row_scale_out,
+                          void* values_bf16, void* stream);
+
+/*
+ * w4_fp4_linear -- y = x . w^T with both operands in microscaled 4-bit
+ * floating point (same format), on the block-scaled tcgen05 tensor cores: the
+ * products of codes are scaled by both blocks' scales and accumulated in
+ * binary32; y = bf16(sum * xrow[m] * wrow[n]).  No bias.
+ *
+ * xcodes, xscales, xrow  x [M, K] as w4_fp4_quantize writes it.
+ * wcodes, wscales, wrow  w [N, K] likewise (xrow, wrow: NULL iff W4_FP4_MX).
+ * y_bf16     device bf16 [M, N] out.
+ * flags      0 or W4_LINEAR_STATIC_WEIGHTS.  The kernel is always launched as
+ *            a programmatic dependent launch; with the flag it may read the
+ *            weight's codes and scales before the preceding kernel ends.
+ * A weight tile is read once per 16, 32, 64, 128 or 256 tokens (the smallest
+ * that holds M), K is split over a thread-block cluster of up to 8 CTAs when
+ * there are few tiles; partial sums are added in a fixed order, so a call's
+ * bits depend on its sizes and inputs alone.
+ */
+w4_status w4_fp4_linear(const uint8_t* xcodes, const uint8_t* xscales, const float* xrow, int64_t M,
+                        const uint8_t* wcodes, const uint8_t* wscales, const float* wrow,
+                        int64_t N, int64_t K, int format, void* y_bf16, unsigned flags,
+                        void* stream);
+
+/*
+ * 8-bit paged KV cache: codes with one float32 scale for each page (block of
+ * tokens) and kv head, keys and values apart; a value is code * scale.
+ *
+ * k_codes    device [num_pages, kv_heads, page_size, head_dim] bytes: int8
+ *            (W4_KV8_INT8, codes -127..127) or e4m3 (W4_KV8_E4M3).
+ * v_codes    device [num_pages, kv_heads, head_dim, page_size] bytes (tokens
+ *            contiguous).
+ * k_scales, v_scales  device float32 [num_pages, kv_heads].
+ * head_dim 64 or 128; page_size 16, 32, 64 or 128.
+ *
+ * A sequence's token p lies in page page_table[b][p / page_size].  Page ids,
+ * lengths and row offsets are device data: what lies outside the caller's
+ * buffers is skipped (a sequence with a bad length or row offset counts as
+ * one without new tokens, a bad page id as a page of zeros that is not
+ * written) and recorded in the device error word.
+ */
+#define W4_KV8_INT8 0
+#define W4_KV8_E4M3 1
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  float* k_scales;
+  float* v_scales;
+  int32_t num_pages, kv_heads, page_size, head_dim, format;
+} w4_kv8_cache;
+
+/*
+ * w4_kv8_append -- writes new keys and values into the cache.  For every page
+ * and kv head that new tokens fall into, with a their largest magnitude there
+ * and s0 the page's scale (0 if the page holds no earlier token of the
+ * sequence):
+ *   s = max(s0, up(a / qmax)), qmax 127 (int8) or 448 (e4m3), up the next
+ *       value that bf16 holds;
+ *   new codes = round(x / s); earlier codes = round(code * s0 / s) if s > s0
+ *       (ties to even; all 0 if s = 0).
+ * Appending the same tokens at the same place again changes nothing.
+ *
+ * k_bf16, v_bf16  device bf16 [rows, kv_heads, head_dim], tokens ldk / ldv
+ *            elements apart (multiples of 8): slices of a fused projection's
+ *            output can be passed as they are.
+ * page_table device int32 [batch, max_pages].
+ * seq_lens   device int32 [batch]: tokens in the cache after this call.
+ * starts     device int32 [batch + 1]: sequence b's new tokens are rows
+ *            starts[b] .. starts[b + 1] - 1 and take the last positions of
+ *            its seq_lens[b]; or NULL: one new token each, row b.
+ * max_new    at least the new tokens of any sequence (1 without starts).
+ * Pages that take new tokens must belong to one sequence alone.
+ */
+w4_status w4_kv8_append(const w4_kv8_cache* cache, const void* k_bf16, int64_t ldk,
+                        const void* v_bf16, int64_t ldv, int64_t rows, const int32_t* page_table,
+                        int64_t max_pages, const int32_t* seq_lens, const int32_t* starts,
+                        int64_t batch, int64_t max_new, void* stream);
+
+/*
+ * w4_kv8_attention -- causal attention of each sequence's newest tokens over
+ * the cache (which holds them already): new token i of n at position
+ * p = seq_lens[b] - n + i sees keys 0 .. p,
+ *   out = softmax(scale * q . k) v,
+ * query head h reading kv head h / (q_heads / kv_heads).  A token with p < 0
+ * gets zeros.  Scores, sums and outputs in binary32; probabilities rounded to
+ * fp16 (relative 2^-11), out once to bf16.
+ *
+ * q_bf16     device bf16 [rows, q_heads, head_dim], tokens ldq elements apart
+ *            (a multiple of 8).
+ * out_bf16   device bf16 [rows, q_heads, head_dim]; rows of no sequence are
+ *            left as they were.
+ * Other arguments as w4_kv8_append.  Results do not depend on timing: every
+ * sum has a fixed order for a given call.
+ */
+w4_status w4_kv8_attention(const void* q_bf16, int64_t ldq, int64_t rows, int64_t q_heads,
+                           const w4_kv8_cache* cache, const int32_t* page_table, int64_t max_pages,
+                           const int32_t* seq_lens, const int32_t* starts, int64_t batch,
+                           int64_t max_new, float scale, void* out_bf16, void* stream);
+
+/*
  * w4_device_error -- reads (and with clear != 0 resets) the library's device
  * error word.  Every wait inside the tcgen05 kernels is bounded (about one
  * second); a kernel that gives up records it here and returns early, leaving
- * its outputs undefined but the CUDA context usable.  Synchronize the streams
- * that ran library kernels first.  Returns W4_OK, W4_ERR_DEVICE_TIMEOUT or
- * W4_ERR_CUDA; *code_out (may be NULL) receives the raw word (0 = none).
+ * its outputs undefined but the CUDA context usable.  The KV cache kernels
+ * record page ids, lengths and offsets that they skipped.  Synchronize the
+ * streams that ran library kernels first.  Returns W4_OK,
+ * W4_ERR_DEVICE_TIMEOUT (a wait gave up), W4_ERR_DEVICE_INDEX (only skipped
+ * indexes) or W4_ERR_CUDA; *code_out (may be NULL) receives the raw word
+ * (0 = none).
  */
 w4_status w4_device_error(int clear, uint32_t* code_out);
 

@@ -1,0 +1,415 @@
+"""GPU parity of the microscaled 4-bit floating-point quantization and linear,
+and of appending to and attention over the 8-bit paged KV cache, against the
+binary64 oracle on identical inputs.
+
+Bars:
+  * quantization and appending: every code, scale and value bit-exact;
+  * linear: |y - ref| <= 2^-8 |ref| + (K/64 + 64) 2^-23 S + tiny, with
+    S = sum_k |x||w|: one rounding to bf16 (at most half a step, 2^-8 of the
+    value); K/64 binary32 accumulations that may each lose a unit of 2^-23 of
+    a partial sum (<= S), and within one of them 64 products aligned to the
+    largest, each losing at most such a unit;
+  * attention: |o - ref| <= 2^-8 |ref| + (2^-11 + 2^-18 + 2 delta) W + A with
+    W = sum_j p_j |v_j| and delta = (d/16 + 24) 2^-23 max_j scale sum |q||k_j|:
+    the rounding to bf16, the probabilities' rounding to fp16 (2^-11), binary32
+    sums and exponentials (2^-18), and the scores' binary32 error, which moves
+    a probability and the normalizer by at most delta each.
+    A = keys 2^-39 V, V the largest magnitude that any page's value scale can
+    hold: a weighted probability is kept times 2^14 in units of the largest
+    value scale, and fp16's spacing under 2^-14 is 2^-24, so each of the
+    smallest is off by at most 2^-25 2^-14 of that (the normalizer is at least
+    the largest probability, 1 in these units).
+"""
+import numpy as np
+import pytest
+import torch
+
+import weight_only_int4_quantize_b200 as w4
+from oracle import lowp_oracle as L
+from weight_only_int4_quantize_b200 import synth
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+DEV = "cuda:0"
+FMTS = ["mx", "nv"]
+KV = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    yield
+    torch.cuda.synchronize()
+    assert w4.device_error(clear=True) == 0
+
+
+# -------------------------------------------------------------- quantize ----
+
+def check_quantize(x, fmt, x_dev=None):
+    codes, scales, row, values = w4.fp4_quantize(x.to(DEV) if x_dev is None else x_dev, fmt,
+                                                 values=True)
+    plain = w4.fp4_quantize(x.to(DEV) if x_dev is None else x_dev, fmt)
+    torch.cuda.synchronize()
+    oc, ob, orow, ov = L.fp4_quantize(synth.bits(x), fmt)
+    assert np.array_equal(codes.cpu().numpy(), L.fp4_pack(oc)), "codes differ"
+    r, blocks = ob.shape
+    i, j = np.arange(r)[:, None], np.arange(blocks)[None, :]
+    assert np.array_equal(L.fp4_scale_byte(scales.cpu().numpy(), i, j), ob), "scales differ"
+    if fmt == "nv":
+        assert np.array_equal(row.cpu().numpy().astype(np.float64), orow)
+    else:
+        assert row is None
+    # A value has at most 6 significant bits, so bf16 holds it unless it lies
+    # under 2^-126, where bf16's spacing is 2^-133 and values go down to 2^-136.
+    held = torch.from_numpy(ov).float().to(torch.bfloat16).double().numpy()
+    assert np.array_equal(held[np.abs(ov) >= 2.0 ** -126], ov[np.abs(ov) >= 2.0 ** -126])
+    assert np.array_equal(values.cpu().double().numpy(), held), "values differ"
+    assert torch.equal(plain[0], codes)  # without values: the same codes
+    return codes, scales, row
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("r,k", [(1, 128), (1, 2048), (3, 384), (33, 1024), (129, 1152),
+                                 (200, 256), (7, 5120), (5, 17408), (300, 4096), (2, 33920)])
+def test_quantize_bit_exact(fmt, r, k):
+    check_quantize(synth.normal_weight(r, k, 0.02, seed=r + k, n_outliers=max(1, k // 100),
+                                       outlier_scale=20.0), fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_ties_and_extremes(fmt):
+    """Values on and next to every rounding border, at scales from the
+    smallest subnormals to the largest bf16, zero rows and blocks, -0."""
+    g = torch.Generator().manual_seed(5)
+    ints = torch.randint(-255, 256, (64, 512), generator=g).float()
+    rows = [ints * 2.0 ** e for e in (-135, -133, -126, -60, -8, 0, 40, 118)]
+    grid = torch.tensor([0.25, 0.5, 0.75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 7, -0.0])
+    on = grid.repeat(32)[None, :] * 2.0 ** torch.arange(-20, 20).float()[:, None]
+    near = on * (1 + torch.randint(-1, 2, on.shape, generator=g) * 2.0 ** -7)
+    scaled = torch.randint(128, 256, (64, 32, 1), generator=g).float() / 128
+    mixed = (torch.randint(0, 29, (64, 32, 16), generator=g) / 4 * scaled).reshape(64, 512)
+    wide = torch.randn(64, 512, generator=g) * 2.0 ** torch.randint(-40, 1, (64, 512), generator=g)
+    zero = torch.zeros(3, 512)
+    zero[1, 300] = 1.0
+    x = torch.cat(rows + [on, near, mixed, wide, zero, -zero]).to(torch.bfloat16)
+    x[-1, 5] = 3.3e38
+    check_quantize(x, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_strided_rows(fmt):
+    wide = synth.normal_activations(37, 3 * 640, seed=9).to(DEV)
+    part = wide[:, 640:1280]
+    check_quantize(part.cpu().contiguous(), fmt, x_dev=part)
+
+
+# ---------------------------------------------------------------- linear ----
+
+def fp4_weight(n, k, fmt, seed):
+    w = synth.normal_weight(n, k, 0.02, seed=seed, n_outliers=max(1, k // 128), outlier_scale=10.0)
+    oc, ob, orow, ov = L.fp4_quantize(synth.bits(w), fmt)
+    return w4.fp4_quantize(w.to(DEV), fmt), ov
+
+
+def linear_bound(ref, xv, wv):
+    k = xv.shape[1]
+    s = np.abs(xv) @ np.abs(wv).T
+    return 2.0 ** -8 * np.abs(ref) + (k / 64 + 64) * 2.0 ** -23 * s + 1e-38
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m,n,k", [
+    (1, 1, 128), (1, 128, 256), (1, 2048, 2048), (2, 129, 384), (7, 1000, 1152), (16, 127, 640),
+    (17, 300, 2176), (32, 256, 128), (33, 64, 896), (64, 333, 1024), (65, 130, 256),
+    (128, 260, 512), (129, 128, 384), (200, 515, 1152), (256, 1001, 256), (257, 96, 128),
+    (300, 384, 4096), (513, 2049, 640), (1, 5120, 17408), (13, 640, 17408), (1999, 200, 512)])
+def test_linear(fmt, m, n, k):
+    (wc, ws, wr), wv = fp4_weight(n, k, fmt, seed=n + k)
+    x = synth.normal_activations(m, k, seed=m + 3)
+    _, _, _, xv = L.fp4_quantize(synth.bits(x), fmt)
+    xc, xs, xr = w4.fp4_quantize(x.to(DEV), fmt)
+    y = w4.fp4_linear(xc, xs, xr, wc, ws, wr, fmt)
+    torch.cuda.synchronize()
+    ref = xv @ wv.T
+    err = np.abs(y.cpu().double().numpy() - ref)
+    assert np.all(err <= linear_bound(ref, xv, wv))
+    again = w4.fp4_linear(xc, xs, xr, wc, ws, wr, fmt, flags=w4.LINEAR_STATIC_WEIGHTS)
+    assert torch.equal(y, again)  # and the same bits on every run
+
+
+def test_linear_any_row_scales_and_padding_bytes():
+    """Row scales that no quantizer of ours writes, and NaN scale bytes in the
+    unused rows of the last tiles: neither disturbs a stored output."""
+    m, n, k = 5, 70, 512
+    (wc, ws, wr), wv = fp4_weight(n, k, "nv", seed=1)
+    x = synth.normal_activations(m, k, seed=2)
+    xc, xs, xr = w4.fp4_quantize(x.to(DEV), "nv")
+    _, _, orow, xv = L.fp4_quantize(synth.bits(x), "nv")
+    i = torch.arange(128, device=DEV)
+    for tiles, rows in ((xs, m), (ws, n)):
+        for j in range(4):
+            at = (i[rows:] % 32) * 16 + i[rows:] // 32 * 4 + j
+            tiles[0][:, at] = 0x7F
+    f = torch.rand(n, generator=torch.Generator().manual_seed(3)) + 0.5
+    y = w4.fp4_linear(xc, xs, xr * 0.37, wc, ws, (wr.cpu() * f).to(DEV), "nv")
+    torch.cuda.synchronize()
+    fx = np.float64(np.float32(0.37))
+    ref = (xv * fx) @ (wv * f.double().numpy()[:, None]).T
+    # two more binary32 products per side
+    bound = linear_bound(ref, xv * fx, wv * f.double().numpy()[:, None]) + 4 * 2.0 ** -24 * np.abs(ref)
+    assert np.all(np.abs(y.cpu().double().numpy() - ref) <= bound)
+
+
+# ----------------------------------------------------------------- cache ----
+
+class Problem:
+    """A paged cache of arbitrary bytes, filled through the oracle's appends."""
+
+    def __init__(self, fmt, heads, d, page, lens, news, q_heads, seed, spare_pages=3, pad_rows=0,
+                 ragged_scale=1.0):
+        g = torch.Generator().manual_seed(seed)
+        self.fmt, self.heads, self.d, self.page, self.q_heads = fmt, heads, d, page, q_heads
+        self.lens, self.news = np.array(lens), np.array(news)
+        used = [-(-int(x) // page) for x in lens]
+        total = sum(used) + spare_pages
+        order = torch.randperm(total, generator=g).tolist()
+        width = max(max(used), 1) + 1
+        self.table = np.full((len(lens), width), -7, np.int32)  # never read behind a sequence
+        for b, u in enumerate(used):
+            for j in range(u):
+                self.table[b, j] = order.pop()
+        self.starts = np.concatenate([[0], np.cumsum(news)]).astype(np.int64)
+        t = int(self.starts[-1]) + pad_rows
+        # queries, keys and values are slices of one projection's rows
+        width = (q_heads + 2 * heads) * d
+        self.qkv = torch.randn(t, width, generator=g)
+        self.qkv[:, q_heads * d:] *= ragged_scale ** torch.randint(-2, 3, (t, 1), generator=g)
+        self.qkv = self.qkv.to(torch.bfloat16)
+        raw = torch.randint(0, 256, (2, total, heads, page, d), generator=g, dtype=torch.uint8)
+        if fmt == "int8":
+            raw[raw == 128] = 0
+        self.kc = raw[0].numpy().copy()
+        self.vc = raw[1].numpy().copy().reshape(total, heads, d, page)
+        sc = (torch.rand(2, total, heads, generator=g) * 0.05 + 0.002).to(torch.bfloat16)
+        if fmt == "e4m3":
+            sc = (sc.float() / 4).to(torch.bfloat16)
+        self.ks, self.vs = sc.double().numpy()
+        if fmt == "e4m3":  # what a sequence holds is a number; anything may lie behind it
+            self._no_nan(self.kc, False)
+            self._no_nan(self.vc, True)
+
+    def _no_nan(self, codes, turned):
+        nan = (codes & 0x7F) == 0x7F
+        keep = np.zeros_like(nan)
+        for b, ln in enumerate(self.lens):
+            for j in range(-(-int(ln) // self.page)):
+                cell = keep[self.table[b, j]]
+                cell = cell.swapaxes(1, 2) if turned else cell
+                cell[:, : min(self.page, int(ln) - j * self.page)] = True
+        codes[nan & keep] = 0x38
+
+    def part(self, lo, hi):
+        d = self.d
+        x = self.qkv.to(DEV)
+        return x[:, lo * d: hi * d].view(x.shape[0], hi - lo, d)
+
+    def host(self, lo, hi):
+        d = self.d
+        return self.qkv[:, lo * d: hi * d].double().numpy().reshape(-1, hi - lo, d)
+
+    def cache(self):
+        return w4.KV8Cache(torch.from_numpy(self.kc).to(DEV).view(KV[self.fmt]),
+                           torch.from_numpy(self.vc).to(DEV).view(KV[self.fmt]),
+                           torch.from_numpy(self.ks).float().to(DEV),
+                           torch.from_numpy(self.vs).float().to(DEV))
+
+    def batch(self, with_starts=True):
+        table = torch.from_numpy(self.table).to(DEV)
+        lens = torch.from_numpy(self.lens.astype(np.int32)).to(DEV)
+        if not with_starts:
+            return table, lens
+        return table, lens, torch.from_numpy(self.starts.astype(np.int32)).to(DEV), \
+            max(1, int(self.news.max()))
+
+    def check_append(self, cache=None):
+        hq, h = self.q_heads, self.heads
+        cache = self.cache() if cache is None else cache
+        want = L.kv_append(self.kc, self.vc, self.ks, self.vs, self.host(hq, hq + h),
+                           self.host(hq + h, hq + 2 * h), self.table, self.lens, self.starts,
+                           self.page, self.fmt)
+        for _ in range(2):  # the second time changes nothing
+            w4.kv8_append(cache, self.part(hq, hq + h), self.part(hq + h, hq + 2 * h), *self.batch())
+            torch.cuda.synchronize()
+            got = [x.view(torch.uint8).cpu().numpy() for x in cache[:2]] + \
+                  [x.cpu().double().numpy() for x in cache[2:]]
+            for name, a, b in zip(("k codes", "v codes", "k scales", "v scales"), got, want):
+                assert np.array_equal(a, b), name
+        self.kc, self.vc, self.ks, self.vs = want
+        return cache
+
+    def check_attention(self, cache=None, scale=None, with_starts=True):
+        cache = self.cache() if cache is None else cache
+        out = torch.full((self.qkv.shape[0], self.q_heads, self.d), 7.0, dtype=torch.bfloat16,
+                         device=DEV)
+        got = w4.kv8_attention(self.part(0, self.q_heads), cache, *self.batch(with_starts),
+                               scale=scale, out=out)
+        torch.cuda.synchronize()
+        assert got is out
+        sc = float(np.float32(self.d ** -0.5 if scale is None else scale))
+        ref, weight, reach = L.kv_attention(self.host(0, self.q_heads), self.kc, self.vc, self.ks,
+                                            self.vs, self.table, self.lens, self.starts, self.page,
+                                            self.fmt, sc)
+        got = got.cpu().double().numpy()
+        rows = int(self.starts[-1])
+        assert np.all(got[rows:] == 7.0)  # rows of no sequence are left as they were
+        delta = (self.d / 16 + 24) * 2.0 ** -23 * reach[:rows]
+        bound = 2.0 ** -8 * np.abs(ref[:rows]) + (2.0 ** -11 + 2.0 ** -18 + 2 * delta) * weight[:rows]
+        bound = bound + max(self.lens) * 2.0 ** -39 * self.vs.max() * L.QMAX[self.fmt]
+        err = np.abs(got[:rows] - ref[:rows])
+        assert np.all(err <= bound + 1e-30), float(np.max(err / (bound + 1e-30)))
+        again = w4.kv8_attention(self.part(0, self.q_heads), cache, *self.batch(with_starts),
+                                 scale=scale, out=torch.empty_like(out))
+        assert torch.equal(again[:rows], out[:rows])
+        return out
+
+
+APPENDS = [  # heads, d, page, lens, news
+    (1, 64, 16, [1], [1]), (2, 128, 16, [16, 17, 33], [1, 1, 1]), (2, 128, 64, [70], [70]),
+    (3, 64, 32, [5, 64, 100], [5, 3, 40]), (2, 128, 128, [128, 129, 300], [128, 2, 172]),
+    (1, 128, 32, [40, 0, 7], [9, 0, 7]), (2, 64, 64, [200, 63], [137, 0]),
+    (2, 64, 16, [3], [9]),  # longer than what is held: the first six are not
+]
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,d,page,lens,news", APPENDS)
+def test_append_bit_exact(fmt, heads, d, page, lens, news):
+    Problem(fmt, heads, d, page, lens, news, q_heads=heads, seed=sum(lens) + page,
+            pad_rows=3).check_append()
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+def test_append_growing_scales_and_zeros(fmt):
+    """Token by token with magnitudes over 2^+-8, so that pages are rescaled
+    again and again, and pages that hold only zeros."""
+    p = Problem(fmt, 2, 64, 16, [16, 41], [1, 1], q_heads=2, seed=4)
+    for step in range(12):
+        p.lens = np.array([5 + step, 30 + step])
+        g = torch.Generator().manual_seed(100 + step)
+        p.qkv = (torch.randn(p.qkv.shape, generator=g) * 2.0 ** (step % 5 * 2 - 4)).to(torch.bfloat16)
+        if step == 3:
+            p.qkv.zero_()
+        p.check_append()
+    z = Problem(fmt, 1, 64, 16, [20], [20], q_heads=1, seed=5)
+    z.qkv.zero_()
+    z.check_append()
+    z.check_attention()
+
+
+ATTENTION = [  # heads, q_heads, d, page, lens, news
+    (1, 1, 64, 16, [1], [1]), (2, 4, 64, 16, [300, 17, 16, 64, 65], [1] * 5),
+    (2, 16, 128, 64, [1, 63, 64, 129, 1000], [1] * 5), (8, 16, 128, 64, [2000], [1]),
+    (1, 32, 128, 32, [500, 31], [1, 1]), (3, 3, 128, 128, [127, 128, 700], [1] * 3),
+    (2, 10, 64, 32, [40, 5], [1, 1]), (2, 4, 128, 16, [100, 20, 0, 9], [7, 20, 0, 1]),
+    (1, 7, 64, 64, [200, 90], [33, 90]), (2, 2, 128, 32, [300], [150]),
+    (2, 4, 64, 16, [3, 10], [9, 2]),  # tokens in front of position 0 see nothing
+    (1, 2, 128, 128, [513, 255], [200, 255]),
+]
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,q_heads,d,page,lens,news", ATTENTION)
+def test_attention(fmt, heads, q_heads, d, page, lens, news):
+    p = Problem(fmt, heads, d, page, lens, news, q_heads, seed=sum(lens) + d, pad_rows=2)
+    p.check_attention()
+
+
+def test_attention_single_tokens_without_starts():
+    p = Problem("int8", 2, 128, 64, [70, 3, 500], [1, 1, 1], 8, seed=3)
+    a = p.check_attention(with_starts=False)
+    assert torch.equal(a, p.check_attention())
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+def test_attention_scales_spread(fmt):
+    """Pages whose value scales differ by 2^10 and key scales that make the
+    softmax all but one-hot; queries of very different magnitude."""
+    p = Problem(fmt, 2, 128, 16, [333, 90], [1, 40], 8, seed=8)
+    e = np.random.RandomState(1).randint(-5, 6, p.vs.shape)
+    p.vs = p.vs * 2.0 ** e
+    p.ks = p.ks * 8
+    mult = 2.0 ** torch.randint(-30, 4, (p.qkv.shape[0], 1), generator=torch.Generator().manual_seed(2))
+    p.qkv = (p.qkv.float() * mult).to(torch.bfloat16)
+    p.check_attention()
+
+
+def test_decode_steps_together():
+    """A prompt and then single tokens through quantize, linear, append and
+    attention, as a decoder layer's attention block runs them, on a stream of
+    its own and replayed from a graph, against the same steps in binary64."""
+    hid, hq, h, d, page, fmt = 512, 8, 4, 64, 16, "nv"
+    n_qkv = (hq + 2 * h) * d
+    (wc, ws, wr), wv = fp4_weight(n_qkv, hid, fmt, seed=31)
+    (oc, os_, or_), ov = fp4_weight(hid, hq * d, fmt, seed=32)
+    prompt = [21, 40]
+    steps = 3
+    cache = w4.kv8_cache(16, h, page, d, device=DEV)
+    table = torch.arange(10, dtype=torch.int32).view(2, 5).to(DEV)
+    kc, vc = (c.view(torch.uint8).cpu().numpy() for c in cache[:2])
+    ks, vs = (c.cpu().double().numpy() for c in cache[2:])
+    stream = torch.cuda.Stream(DEV)
+    lens = np.zeros(2, np.int64)
+    x_buf = lens_buf = graph = y = None
+    for step in range(steps + 1):
+        news = np.array(prompt if step == 0 else [1, 1])
+        starts = np.concatenate([[0], np.cumsum(news)])
+        lens = lens + news
+        x = synth.normal_activations(int(starts[-1]), hid, seed=40 + step)
+
+        def layer(x, lens_t, starts_t, most):
+            qkv = w4.fp4_linear(*w4.fp4_quantize(x, fmt), wc, ws, wr, fmt)
+            q = qkv[:, : hq * d].view(-1, hq, d)
+            k = qkv[:, hq * d: (hq + h) * d].view(-1, h, d)
+            v = qkv[:, (hq + h) * d:].view(-1, h, d)
+            w4.kv8_append(cache, k, v, table, lens_t, starts_t, most)
+            o = w4.kv8_attention(q, cache, table, lens_t, starts_t, most)
+            return qkv, o, w4.fp4_linear(*w4.fp4_quantize(o.view(-1, hq * d), fmt), oc, os_, or_, fmt)
+
+        lens_t = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        if step < 2:
+            starts_t = torch.tensor(starts, dtype=torch.int32, device=DEV)
+            stream.wait_stream(torch.cuda.current_stream())
+            xd = x.to(DEV)
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                qkv, o, y = layer(xd, lens_t, starts_t, int(news.max()))
+            stream.synchronize()
+        else:
+            if graph is None:
+                x_buf, lens_buf = x.to(DEV), lens_t.clone()
+                graph = torch.cuda.CUDAGraph()
+                torch.cuda.synchronize()
+                with torch.cuda.graph(graph):
+                    qkv, o, y = layer(x_buf, lens_buf, None, None)
+            x_buf.copy_(x.to(DEV))
+            lens_buf.copy_(lens_t)
+            graph.replay()
+            torch.cuda.synchronize()
+        xv = L.fp4_quantize(synth.bits(x), fmt)[3]
+        ref = xv @ wv.T
+        got = qkv.cpu()
+        assert np.all(np.abs(got.double().numpy() - ref) <= linear_bound(ref, xv, wv))
+        # each further step from the bits that the one before it wrote
+        part = got.double().numpy().reshape(-1, hq + 2 * h, d)
+        kc, vc, ks, vs = L.kv_append(kc, vc, ks, vs, part[:, hq: hq + h], part[:, hq + h:],
+                                     table.cpu().numpy(), lens, starts, page, "int8")
+        assert np.array_equal(cache.k_codes.view(torch.uint8).cpu().numpy(), kc)
+        assert np.array_equal(cache.v_codes.view(torch.uint8).cpu().numpy(), vc)
+        ro, weight, reach = L.kv_attention(part[:, :hq], kc, vc, ks, vs, table.cpu().numpy(), lens,
+                                           starts, page, "int8", d ** -0.5)
+        delta = (d / 16 + 24) * 2.0 ** -23 * reach
+        bound = 2.0 ** -8 * np.abs(ro) + (2.0 ** -11 + 2.0 ** -18 + 2 * delta) * weight
+        assert np.all(np.abs(o.cpu().double().numpy() - ro) <= bound + 1e-30)
+        oq = L.fp4_quantize(synth.bits(o.cpu().view(-1, hq * d)), fmt)[3]
+        ry = oq @ ov.T
+        assert np.all(np.abs(y.cpu().double().numpy() - ry) <= linear_bound(ry, oq, ov))

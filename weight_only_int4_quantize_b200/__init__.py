@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 __all__ = [
     "W4Error", "lib", "quantize_pack", "quantize_pack_batched", "quantize_pack_rows",
@@ -22,6 +22,8 @@ __all__ = [
     "awq_workspace_bytes", "device_error", "selftest_bounded_wait",
     "LINEAR_FORCE_GEMV", "LINEAR_FORCE_GEMM", "LINEAR_PDL", "LINEAR_STATIC_WEIGHTS",
     "LINEAR_DECODE_STREAM", "LINEAR_DECODE_TILED", "STREAM_BATCH",
+    "fp4_quantize", "fp4_linear", "fp4_scale_shape", "FP4_FORMATS",
+    "KV8Cache", "kv8_cache", "kv8_append", "kv8_attention",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw4.so")
@@ -39,6 +41,7 @@ STREAM_BATCH = 256
 _STATUS = {
     0: "W4_OK", 1: "W4_ERR_INVALID_ARG", 2: "W4_ERR_SHAPE", 3: "W4_ERR_ALIGNMENT",
     4: "W4_ERR_UNSUPPORTED", 5: "W4_ERR_WORKSPACE", 6: "W4_ERR_CUDA", 7: "W4_ERR_DEVICE_TIMEOUT",
+    8: "W4_ERR_DEVICE_INDEX",
 }
 
 
@@ -115,6 +118,18 @@ def _declare(L: ctypes.CDLL) -> None:
     L.awq_block_search.restype = ctypes.c_int
     L.awq_block_search.argtypes = [_p, _p, _i64, _p, _p, _p, ctypes.c_int, _p, ctypes.c_int,
                                    ctypes.c_int, _p, _p, _p, ctypes.c_size_t, _p]
+    L.w4_fp4_scale_bytes.restype = ctypes.c_size_t
+    L.w4_fp4_scale_bytes.argtypes = [_i64, _i64, ctypes.c_int]
+    L.w4_fp4_quantize.restype = ctypes.c_int
+    L.w4_fp4_quantize.argtypes = [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p, _p, _p, _p]
+    L.w4_fp4_linear.restype = ctypes.c_int
+    L.w4_fp4_linear.argtypes = [_p, _p, _p, _i64, _p, _p, _p, _i64, _i64, ctypes.c_int, _p,
+                                ctypes.c_uint, _p]
+    L.w4_kv8_append.restype = ctypes.c_int
+    L.w4_kv8_append.argtypes = [_p, _p, _i64, _p, _i64, _i64, _p, _i64, _p, _p, _i64, _i64, _p]
+    L.w4_kv8_attention.restype = ctypes.c_int
+    L.w4_kv8_attention.argtypes = [_p, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _i64, _i64,
+                                   ctypes.c_float, _p, _p]
     L.w4_device_error.restype = ctypes.c_int
     L.w4_device_error.argtypes = [ctypes.c_int, _p]
     L.w4_selftest_bounded_wait.restype = ctypes.c_int
@@ -663,11 +678,234 @@ def awq_block_search(x, block, next_block, alphas, shrinks, symmetric: bool, cfg
     return choice, losses
 
 
+# Formats of fp4_quantize / fp4_linear: (C constant, input channels per block scale).
+FP4_FORMATS = {"mx": (0, 32), "nv": (1, 16)}
+
+
+def _fp4_format(fmt):
+    if fmt not in FP4_FORMATS:
+        raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {fmt!r}")
+    return FP4_FORMATS[fmt]
+
+
+def fp4_scale_shape(rows: int, k: int, fmt: str):
+    """Shape of the uint8 scale tiles of a [rows, k] matrix."""
+    _, block = _fp4_format(fmt)
+    return ((rows + 127) // 128, k // (4 * block), 512)
+
+
+def _rows_of(t, width, name):
+    """Elements between the rows of a tensor whose rows (everything but the
+    first axis) are contiguous: slices of a wider buffer's rows are allowed."""
+    inner = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"{name}: only the first axis may be strided")
+        inner *= size
+    if t.shape[0] > 1 and t.stride(0) < width:
+        raise ValueError(f"{name}: rows overlap")
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _cuda_rows(t, dtype, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def fp4_quantize(x, fmt: str = "mx", values: bool = False):
+    """Microscaled 4-bit floating-point codes of a bf16 [R, K] matrix (rows may
+    be slices of a wider buffer's).
+
+    Returns (codes uint8 [R, K/2], scale tiles uint8 [ceil(R/128), blocks/4,
+    512], row scales float32 [R] or None for "mx"), and with values=True also
+    the bf16 [R, K] values that the codes stand for."""
+    torch = _torch()
+    f, block = _fp4_format(fmt)
+    _cuda_rows(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [R, K]")
+    r, k = x.shape
+    ldx = _rows_of(x, k, "x")
+    codes = torch.empty((r, k // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty(fp4_scale_shape(r, k, fmt), dtype=torch.uint8, device=x.device)
+    row = torch.empty((r,), dtype=torch.float32, device=x.device) if fmt == "nv" else None
+    val = torch.empty((r, k), dtype=torch.bfloat16, device=x.device) if values else None
+    with torch.cuda.device(x.device):
+        st = lib().w4_fp4_quantize(x.data_ptr(), r, k, ldx, f, codes.data_ptr(),
+                                   scales.data_ptr(), None if row is None else row.data_ptr(),
+                                   None if val is None else val.data_ptr(), _stream(x.device))
+    _check(st, "w4_fp4_quantize")
+    return (codes, scales, row, val) if values else (codes, scales, row)
+
+
+def fp4_linear(xcodes, xscales, xrow, wcodes, wscales, wrow, fmt: str = "mx", flags: int = 0,
+               out=None):
+    """y = x . w^T, bf16 [M, N], of an activation and a weight in the same
+    microscaled 4-bit format (each as fp4_quantize returns it)."""
+    torch = _torch()
+    f, _ = _fp4_format(fmt)
+    for t, name in ((xcodes, "xcodes"), (xscales, "xscales"), (wcodes, "wcodes"),
+                    (wscales, "wscales")):
+        _cuda(t, torch.uint8, name)
+    if xcodes.dim() != 2 or wcodes.dim() != 2:
+        raise ValueError("xcodes and wcodes must be [rows, K/2]")
+    m, k = xcodes.shape[0], xcodes.shape[1] * 2
+    n = wcodes.shape[0]
+    _expect(wcodes, (n, k // 2), "wcodes")
+    _expect(xscales, fp4_scale_shape(m, k, fmt), "xscales")
+    _expect(wscales, fp4_scale_shape(n, k, fmt), "wscales")
+    for t, rows, name in ((xrow, m, "xrow"), (wrow, n, "wrow")):
+        if (t is None) != (fmt == "mx"):
+            raise ValueError(f"{name} belongs to format 'nv' alone")
+        if t is not None:
+            _cuda(t, torch.float32, name)
+            _expect(t, (rows,), name)
+    if out is not None:
+        _cuda(out, torch.bfloat16, "out")
+        _expect(out, (m, n), "out")
+    _same_device(xcodes, xscales=xscales, xrow=xrow, wcodes=wcodes, wscales=wscales, wrow=wrow,
+                 out=out)
+    y = out if out is not None else torch.empty((m, n), dtype=torch.bfloat16, device=xcodes.device)
+    with torch.cuda.device(xcodes.device):
+        st = lib().w4_fp4_linear(xcodes.data_ptr(), xscales.data_ptr(),
+                                 None if xrow is None else xrow.data_ptr(), m, wcodes.data_ptr(),
+                                 wscales.data_ptr(), None if wrow is None else wrow.data_ptr(), n,
+                                 k, f, y.data_ptr(), int(flags), _stream(xcodes.device))
+    _check(st, "w4_fp4_linear")
+    return y
+
+
+class KV8Cache(NamedTuple):
+    """An 8-bit paged KV cache: codes int8 or float8_e4m3fn, k_codes
+    [pages, kv_heads, page_size, head_dim], v_codes [pages, kv_heads, head_dim,
+    page_size], and float32 scales [pages, kv_heads]."""
+    k_codes: "torch.Tensor"
+    v_codes: "torch.Tensor"
+    k_scales: "torch.Tensor"
+    v_scales: "torch.Tensor"
+
+
+class _KV8Cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
+
+
+def kv8_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=None,
+              device="cuda") -> KV8Cache:
+    """An empty (zeroed) cache; dtype torch.int8 (default) or
+    torch.float8_e4m3fn."""
+    torch = _torch()
+    dtype = torch.int8 if dtype is None else dtype
+    if dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise TypeError("cache codes are int8 or float8_e4m3fn")
+    k = torch.zeros((num_pages, kv_heads, page_size, head_dim), dtype=torch.uint8, device=device)
+    v = torch.zeros((num_pages, kv_heads, head_dim, page_size), dtype=torch.uint8, device=device)
+    s = torch.zeros((2, num_pages, kv_heads), dtype=torch.float32, device=device)
+    return KV8Cache(k.view(dtype), v.view(dtype), s[0].clone(), s[1].clone())
+
+
+def _kv8_args(ref, cache, page_table, seq_lens, starts, max_new):
+    """Checks of what appending and attention share; ref is [rows, heads,
+    head_dim].  Returns the C cache, the batch size and max_new."""
+    torch = _torch()
+    k = cache.k_codes
+    if not isinstance(k, torch.Tensor) or k.dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise TypeError("cache codes must be int8 or float8_e4m3fn")
+    _cuda(k, k.dtype, "k_codes")
+    _cuda(cache.v_codes, k.dtype, "v_codes")
+    if k.dim() != 4:
+        raise ValueError("k_codes must be [pages, kv_heads, page_size, head_dim]")
+    pages, heads, page, d = k.shape
+    _expect(cache.v_codes, (pages, heads, d, page), "v_codes")
+    for t, name in ((cache.k_scales, "k_scales"), (cache.v_scales, "v_scales")):
+        _cuda(t, torch.float32, name)
+        _expect(t, (pages, heads), name)
+    _cuda(page_table, torch.int32, "page_table")
+    _cuda(seq_lens, torch.int32, "seq_lens")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    b = page_table.shape[0]
+    _expect(seq_lens, (b,), "seq_lens")
+    if starts is not None:
+        _cuda(starts, torch.int32, "starts")
+        _expect(starts, (b + 1,), "starts")
+        if max_new is None:
+            raise ValueError("max_new is needed with starts")
+    elif max_new not in (None, 1):
+        raise ValueError("without starts every sequence has one new token")
+    if ref.dim() != 3 or ref.shape[2] != d:
+        raise ValueError(f"new tokens must be [rows, heads, {d}]")
+    _same_device(ref, k_codes=k, v_codes=cache.v_codes, k_scales=cache.k_scales,
+                 v_scales=cache.v_scales, page_table=page_table, seq_lens=seq_lens, starts=starts)
+    c = _KV8Cache(k.data_ptr(), cache.v_codes.data_ptr(), cache.k_scales.data_ptr(),
+                  cache.v_scales.data_ptr(), pages, heads, page, d,
+                  0 if k.dtype == torch.int8 else 1)
+    return c, b, 1 if max_new is None else int(max_new)
+
+
+def kv8_append(cache, k, v, page_table, seq_lens, starts=None, max_new=None) -> None:
+    """Writes new keys and values (bf16 [rows, kv_heads, head_dim]; only the
+    token axis may be strided) into the cache's pages.  seq_lens int32 [batch]
+    counts the new tokens; starts int32 [batch + 1] gives each sequence's rows
+    (with max_new, at least the most of any), None one token each."""
+    torch = _torch()
+    _cuda_rows(k, torch.bfloat16, "k")
+    _cuda_rows(v, torch.bfloat16, "v")
+    c, b, most = _kv8_args(k, cache, page_table, seq_lens, starts, max_new)
+    _expect(k, (k.shape[0], c.kv_heads, c.head_dim), "k")
+    _expect(v, tuple(k.shape), "v")
+    _same_device(k, v=v)
+    width = c.kv_heads * c.head_dim
+    ldk, ldv = _rows_of(k, width, "k"), _rows_of(v, width, "v")
+    with torch.cuda.device(k.device):
+        st = lib().w4_kv8_append(ctypes.byref(c), k.data_ptr(), ldk, v.data_ptr(), ldv, k.shape[0],
+                                 page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
+                                 None if starts is None else starts.data_ptr(), b, most,
+                                 _stream(k.device))
+    _check(st, "w4_kv8_append")
+
+
+def kv8_attention(q, cache, page_table, seq_lens, starts=None, max_new=None, scale=None, out=None):
+    """Causal attention of the newest tokens q (bf16 [rows, q_heads, head_dim],
+    only the token axis may be strided) over the cache, which holds them
+    already; other arguments as kv8_append.  scale: 1/sqrt(head_dim) if None.
+    Returns bf16 [rows, q_heads, head_dim]; rows of no sequence are not
+    written."""
+    torch = _torch()
+    _cuda_rows(q, torch.bfloat16, "q")
+    c, b, most = _kv8_args(q, cache, page_table, seq_lens, starts, max_new)
+    rows, heads, d = q.shape
+    ldq = _rows_of(q, heads * d, "q")
+    if out is not None:
+        _cuda(out, torch.bfloat16, "out")
+        _expect(out, (rows, heads, d), "out")
+        _same_device(q, out=out)
+    o = out if out is not None else torch.empty((rows, heads, d), dtype=torch.bfloat16,
+                                                device=q.device)
+    with torch.cuda.device(q.device):
+        st = lib().w4_kv8_attention(q.data_ptr(), ldq, rows, heads, ctypes.byref(c),
+                                    page_table.data_ptr(), page_table.shape[1],
+                                    seq_lens.data_ptr(),
+                                    None if starts is None else starts.data_ptr(), b, most,
+                                    float(d ** -0.5 if scale is None else scale), o.data_ptr(),
+                                    _stream(q.device))
+    _check(st, "w4_kv8_attention")
+    return o
+
+
 def device_error(clear: bool = True) -> int:
-    """The library's device error word (0 = no kernel gave up on a wait)."""
+    """The library's device error word (0 = no kernel gave up on a wait or
+    skipped an index outside its buffers)."""
     code = ctypes.c_uint32(0)
     st = lib().w4_device_error(int(bool(clear)), ctypes.byref(code))
-    if st not in (0, 7):
+    if st not in (0, 7, 8):
         _check(st, "w4_device_error")
     return int(code.value)
 

@@ -9,6 +9,8 @@
 #include <vector>
 
 #include "w4.h"
+#include "fp4.cuh"
+#include "kv8.cuh"
 #include "w4_common.cuh"
 #include "w4_kernels.h"
 
@@ -152,6 +154,7 @@ const char* w4_status_string(w4_status s) {
     case W4_ERR_WORKSPACE: return "workspace missing or too small";
     case W4_ERR_CUDA: return "CUDA runtime error";
     case W4_ERR_DEVICE_TIMEOUT: return "a kernel gave up on a bounded wait";
+    case W4_ERR_DEVICE_INDEX: return "a kernel met an index outside the caller's buffers";
   }
   return "unknown status";
 }
@@ -923,6 +926,137 @@ w4_status awq_score_grid_static_scratch(const void* x_bf16, int64_t M, const voi
                         W4_AWQ_STATIC_SCRATCH_BYTES, stream);
 }
 
+static bool valid_fp4_format(int format) { return format == W4_FP4_MX || format == W4_FP4_NV; }
+
+size_t w4_fp4_scale_bytes(int64_t R, int64_t K, int format) {
+  if (R < 1 || R > 0x7FFFFFFF || !valid_k(K) || !valid_fp4_format(format)) return 0;
+  return static_cast<size_t>((R + 127) / 128) * (K / (4 * fp4_block(format))) * 512;
+}
+
+w4_status w4_fp4_quantize(const void* x_bf16, int64_t R, int64_t K, int64_t ldx, int format,
+                          uint8_t* codes_out, uint8_t* scales_out, float* row_scale_out,
+                          void* values_bf16, void* stream) {
+  if (!x_bf16 || !codes_out || !scales_out) return W4_ERR_INVALID_ARG;
+  if (!valid_fp4_format(format)) return W4_ERR_UNSUPPORTED;
+  if ((format == W4_FP4_NV) != (row_scale_out != nullptr)) return W4_ERR_INVALID_ARG;
+  if (R < 1 || R > 0x7FFFFFFF || !valid_k(K) || R > (int64_t{1} << 40) / K || ldx < K)
+    return W4_ERR_SHAPE;
+  if (!aligned16(x_bf16) || ldx % 8 != 0 || !aligned16(codes_out) || !aligned16(scales_out) ||
+      (row_scale_out && !aligned16(row_scale_out)) || (values_bf16 && !aligned16(values_bf16)))
+    return W4_ERR_ALIGNMENT;
+  int sms = 0;
+  const w4_status st = device_info(&sms, nullptr);
+  if (st != W4_OK) return st;
+  return cuda_status(launch_fp4_quantize(x_bf16, R, K, ldx, format, codes_out, scales_out,
+                                         row_scale_out, values_bf16,
+                                         static_cast<cudaStream_t>(stream), sms),
+                     "fp4 quantize launch");
+}
+
+w4_status w4_fp4_linear(const uint8_t* xcodes, const uint8_t* xscales, const float* xrow, int64_t M,
+                        const uint8_t* wcodes, const uint8_t* wscales, const float* wrow,
+                        int64_t N, int64_t K, int format, void* y_bf16, unsigned flags,
+                        void* stream) {
+  if (!xcodes || !xscales || !wcodes || !wscales || !y_bf16) return W4_ERR_INVALID_ARG;
+  if (flags & ~W4_LINEAR_STATIC_WEIGHTS) return W4_ERR_INVALID_ARG;
+  if (!valid_fp4_format(format)) return W4_ERR_UNSUPPORTED;
+  if ((format == W4_FP4_NV) != (xrow != nullptr) || (format == W4_FP4_NV) != (wrow != nullptr))
+    return W4_ERR_INVALID_ARG;
+  if (M < 1 || N < 1 || !valid_k(K) || M > 0x7FFFFFFF - 256 || N > 0x7FFFFFFF - 256)
+    return W4_ERR_SHAPE;
+  if (!aligned16(xcodes) || !aligned16(xscales) || !aligned16(wcodes) || !aligned16(wscales) ||
+      !aligned16(y_bf16) || (xrow && !aligned16(xrow)) || (wrow && !aligned16(wrow)))
+    return W4_ERR_ALIGNMENT;
+  int sms = 0;
+  unsigned* err = nullptr;
+  const w4_status st = device_info(&sms, &err);
+  if (st != W4_OK) return st;
+  return cuda_status(
+      launch_fp4_linear(xcodes, xscales, xrow, static_cast<int>(M), wcodes, wscales, wrow,
+                        static_cast<int>(N), static_cast<int>(K), format, y_bf16,
+                        (flags & W4_LINEAR_STATIC_WEIGHTS) != 0, static_cast<cudaStream_t>(stream),
+                        sms, err),
+      "fp4 linear launch");
+}
+
+// Arguments that appending and attention share.
+static w4_status check_kv8(const w4_kv8_cache* c, const int32_t* page_table, int64_t max_pages,
+                           const int32_t* seq_lens, const int32_t* starts, int64_t batch,
+                           int64_t rows, int64_t max_new, Kv8Cache* cache, Kv8Batch* bt) {
+  if (!c || !page_table || !seq_lens) return W4_ERR_INVALID_ARG;
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return W4_ERR_INVALID_ARG;
+  if (c->format != W4_KV8_INT8 && c->format != W4_KV8_E4M3) return W4_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128) return W4_ERR_UNSUPPORTED;
+  int log_page = 0;
+  while (log_page < 8 && (1 << log_page) != c->page_size) ++log_page;
+  if (log_page < 4 || log_page > 7) return W4_ERR_UNSUPPORTED;
+  if (c->num_pages < 1 || c->kv_heads < 1 || max_pages < 1 || batch < 1 || rows < 1 ||
+      max_new < 1 || c->kv_heads > 65535 || rows > 0x7FFFFFFF ||
+      max_pages > 0x40000000 >> log_page || batch * c->kv_heads > 0x7FFFFFFF || max_new > rows ||
+      batch > 0x7FFFFFFF)
+    return W4_ERR_SHAPE;
+  if (!starts && (rows != batch || max_new != 1)) return W4_ERR_SHAPE;
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) ||
+      !aligned16(c->v_scales) || (reinterpret_cast<uintptr_t>(page_table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(starts) & 3u))
+    return W4_ERR_ALIGNMENT;
+  *cache = Kv8Cache{static_cast<uint8_t*>(c->k_codes), static_cast<uint8_t*>(c->v_codes),
+                    c->k_scales, c->v_scales, c->num_pages, c->kv_heads, log_page};
+  *bt = Kv8Batch{page_table, seq_lens, starts, static_cast<int>(batch),
+                 static_cast<int>(max_pages), static_cast<int>(rows), static_cast<int>(max_new)};
+  return W4_OK;
+}
+
+w4_status w4_kv8_append(const w4_kv8_cache* cache, const void* k_bf16, int64_t ldk,
+                        const void* v_bf16, int64_t ldv, int64_t rows, const int32_t* page_table,
+                        int64_t max_pages, const int32_t* seq_lens, const int32_t* starts,
+                        int64_t batch, int64_t max_new, void* stream) {
+  if (!k_bf16 || !v_bf16) return W4_ERR_INVALID_ARG;
+  Kv8Cache c;
+  Kv8Batch bt;
+  w4_status st = check_kv8(cache, page_table, max_pages, seq_lens, starts, batch, rows, max_new,
+                           &c, &bt);
+  if (st != W4_OK) return st;
+  const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
+  if (ldk < width || ldv < width) return W4_ERR_SHAPE;
+  // The pages that one sequence's new tokens can touch are a grid dimension.
+  if ((max_new + cache->page_size - 2) / cache->page_size + 1 > 65535) return W4_ERR_UNSUPPORTED;
+  if (!aligned16(k_bf16) || !aligned16(v_bf16) || ldk % 8 != 0 || ldv % 8 != 0)
+    return W4_ERR_ALIGNMENT;
+  int sms = 0;
+  unsigned* err = nullptr;
+  st = device_info(&sms, &err);
+  if (st != W4_OK) return st;
+  return cuda_status(launch_kv8_append(c, bt, k_bf16, v_bf16, ldk, ldv, cache->head_dim,
+                                       cache->format, static_cast<cudaStream_t>(stream), err),
+                     "KV append launch");
+}
+
+w4_status w4_kv8_attention(const void* q_bf16, int64_t ldq, int64_t rows, int64_t q_heads,
+                           const w4_kv8_cache* cache, const int32_t* page_table, int64_t max_pages,
+                           const int32_t* seq_lens, const int32_t* starts, int64_t batch,
+                           int64_t max_new, float scale, void* out_bf16, void* stream) {
+  if (!q_bf16 || !out_bf16) return W4_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return W4_ERR_INVALID_ARG;
+  Kv8Cache c;
+  Kv8Batch bt;
+  w4_status st = check_kv8(cache, page_table, max_pages, seq_lens, starts, batch, rows, max_new,
+                           &c, &bt);
+  if (st != W4_OK) return st;
+  if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_heads > 65536 ||
+      max_new * (q_heads / cache->kv_heads) > 0x7FFFFFFF - 256 || ldq < q_heads * cache->head_dim)
+    return W4_ERR_SHAPE;
+  if (!aligned16(q_bf16) || !aligned16(out_bf16) || ldq % 8 != 0) return W4_ERR_ALIGNMENT;
+  int sms = 0;
+  unsigned* err = nullptr;
+  st = device_info(&sms, &err);
+  if (st != W4_OK) return st;
+  return cuda_status(launch_kv8_attention(c, bt, q_bf16, ldq, static_cast<int>(q_heads),
+                                          cache->head_dim, cache->format, scale, out_bf16,
+                                          static_cast<cudaStream_t>(stream), sms, err),
+                     "KV attention launch");
+}
+
 w4_status w4_device_error(int clear, uint32_t* code_out) {
   unsigned v = 0;
   w4_status st = cuda_status(cudaMemcpyFromSymbol(&v, g_w4_device_error, sizeof(v)),
@@ -935,7 +1069,8 @@ w4_status w4_device_error(int clear, uint32_t* code_out) {
     if (st != W4_OK) return st;
   }
   if (code_out) *code_out = v;
-  return v ? W4_ERR_DEVICE_TIMEOUT : W4_OK;
+  if (v & kErrWaitTimeout) return W4_ERR_DEVICE_TIMEOUT;
+  return v ? W4_ERR_DEVICE_INDEX : W4_OK;
 }
 
 w4_status w4_selftest_bounded_wait(uint64_t limit_ns, void* stream) {

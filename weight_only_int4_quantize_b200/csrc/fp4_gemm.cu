@@ -1,0 +1,488 @@
+// y = x . w^T with both operands in microscaled 4-bit floating point, on the
+// block-scaled tcgen05 tensor cores (kind::mxf4 / kind::mxf4nvf4): the
+// products of e2m1 codes are scaled by their blocks' scales inside the MMA
+// and accumulated in fp32 tensor memory; nothing is dequantized.
+//
+//   y[m, n] = xrow[m] wrow[n] sum_b sx[m, b] sw[n, b] sum_{k in b} cx[m, k] cw[n, k]
+//
+// (the row scales only for nv; applied to the fp32 sum, then one rounding to
+// bf16).
+//
+// The weight is always the A operand (128 output channels per tile) and the
+// tokens the B operand (NB = 16 ... 256 columns), so one kernel serves a
+// single token and a prefill: a decode step streams the weight once through
+// tiles of 16 token columns.  A stage is 256 channels: 128-byte rows of
+// codes (TMA, 128-byte swizzle) and 2 (mx) or 4 (nv) scale tiles of 512
+// bytes per 128 rows, copied to shared memory in one piece and to TMEM by
+// tcgen05.cp, which the tensor pipe runs in order with the MMAs.  A K tail
+// of 128 channels issues half the stage's MMAs.
+//
+// Warp roles: 0 TMA producer, 1 TMEM allocation and MMA issue, 2..5
+// epilogue.  K may be split over a thread-block cluster of up to 8 CTAs (few
+// tiles); the fp32 partial tiles are added through distributed shared memory
+// in rank order, so a launch configuration always gives the same bits.
+// Every wait is bounded; see w4_common.cuh.
+#include <cooperative_groups.h>
+#include <cudaTypedefs.h>
+
+#include "fp4.cuh"
+#include "w4_kernels.h"
+
+namespace w4 {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kFp4Threads = 192;
+constexpr int kRows = 128;       // output channels of a tile
+constexpr int kStageK = 256;     // channels of a stage
+constexpr int kMaxSplit = 8;
+constexpr unsigned kKernelIdFp4 = 8;
+
+template <int FMT, int NB>
+struct Fp4Tile {
+  static constexpr int kColTiles = NB > 128 ? NB / 128 : 1;  // scale tiles across the tokens
+  static constexpr int kWords = fp4_stage_words(FMT);
+  static constexpr uint32_t kABytes = kRows * kStageK / 2;
+  static constexpr uint32_t kBBytes = NB * kStageK / 2;
+  static constexpr uint32_t kSfaBytes = kWords * 512;
+  static constexpr uint32_t kSfbBytes = kColTiles * kWords * 512;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+  // Two CTAs share an SM unless the token tile is 256 wide.
+  static constexpr int kCtasPerSm = NB > 128 ? 1 : 2;
+  static constexpr int kStages =
+      static_cast<int>((kCtasPerSm == 1 ? 222u * 1024u : 109u * 1024u) / kStageBytes);
+  // TMEM: NB accumulator columns, then the scale columns of two stages.
+  static constexpr uint32_t kSfCols = 4 * kWords * (1 + kColTiles);
+  static constexpr uint32_t kUsed = NB + 2 * kSfCols;
+  static constexpr uint32_t kTmemCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static constexpr uint32_t bars = kStages * kStageBytes;
+  static constexpr uint32_t misc = bars + (2 * kStages + 2) * 8;
+  static constexpr size_t bytes = misc + 16 + 1024;  // + alignment
+};
+
+struct Fp4Args {
+  const uint8_t* wscales;
+  const uint8_t* xscales;
+  const float* wrow;
+  const float* xrow;
+  __nv_bfloat16* y;
+  int M, N, K;
+  int m_tiles;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// 32 rows of 16 bytes (unswizzled 8-row core matrices, 128 bytes apart) to
+// 32 TMEM lanes x 4 columns, repeated in all four lane quarters.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;  // SBO
+  d |= static_cast<uint64_t>(1u) << 46;         // descriptor version
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds: e2m1 operands, K-major,
+// M x N, scale ids within a TMEM scale word.
+template <int FMT>
+__device__ __forceinline__ constexpr uint32_t idesc_fp4(int N, int sf_id) {
+  return (static_cast<uint32_t>(sf_id) << 4)       // B scale id
+         | (1u << 7) | (1u << 10)                  // A, B: e2m1
+         | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
+         | ((FMT == kFp4Mx ? 1u : 0u) << 23)       // scales: ue8m0, else ue4m3
+         | (static_cast<uint32_t>(kRows >> 7) << 27)  // M / 128
+         | (static_cast<uint32_t>(sf_id) << 29);   // A scale id
+}
+
+template <int FMT>
+__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (FMT == kFp4Mx)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+template <int FMT, int NB>
+__global__ void __launch_bounds__(kFp4Threads)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
+                    const Fp4Args a, int static_w, unsigned* err) {
+  using T = Fp4Tile<FMT, NB>;
+  constexpr int S = T::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw);
+  auto stage = [&](int s) { return base + static_cast<uint32_t>(s) * T::kStageBytes; };
+  auto full = [&](int s) { return base + T::bars + 8u * s; };
+  auto empty = [&](int s) { return base + T::bars + 8u * (S + s); };
+  const uint32_t acc_full = base + T::bars + 8u * (2 * S);
+  const uint32_t done_bar = acc_full + 8u;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + T::misc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + T::misc + 8);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  int ks, rank;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ks));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int tile = static_cast<int>(blockIdx.x) / ks;
+  const int tile_m = tile % a.m_tiles;  // token tiles of one weight tile run together
+  const int tile_n = tile / a.m_tiles;
+  const int n0 = tile_n * kRows;
+  const int m0 = tile_m * NB;
+  const int all_kb = (a.K + kStageK - 1) / kStageK;
+  const int kb_begin = static_cast<int>(static_cast<int64_t>(rank) * all_kb / ks);
+  const int num_kb = static_cast<int>(static_cast<int64_t>(rank + 1) * all_kb / ks) - kb_begin;
+  // 512-byte scale tiles of one 128-row tile.
+  const int words = a.K / (4 * fp4_block(FMT));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tw);
+    tma_prefetch_desc(&tx);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), T::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA --
+    if (lane == 0) {
+      const int x_tiles = (a.M + 127) / 128;
+      // Scale tiles of local stage kb: fewer where the K tail ends the stage.
+      auto stage_words = [&](int kb) {
+        const int left = words - (kb_begin + kb) * T::kWords;
+        return left < T::kWords ? left : T::kWords;
+      };
+      auto load_w = [&](int kb) {
+        const int s = kb % S;
+        const uint32_t w = static_cast<uint32_t>(stage_words(kb)) * 512u;
+        mbar_arrive_expect_tx(full(s), T::kABytes + T::kBBytes + w * (1 + T::kColTiles));
+        tma_load_2d(stage(s), &tw, (kb_begin + kb) * (kStageK / 2), n0, full(s));
+        bulk_load(stage(s) + T::kABytes + T::kBBytes,
+                  a.wscales + (static_cast<int64_t>(tile_n) * words +
+                               static_cast<int64_t>(kb_begin + kb) * T::kWords) * 512,
+                  w, full(s));
+      };
+      auto load_x = [&](int kb) {
+        const int s = kb % S;
+        const uint32_t w = static_cast<uint32_t>(stage_words(kb)) * 512u;
+        tma_load_2d(stage(s) + T::kABytes, &tx, (kb_begin + kb) * (kStageK / 2), m0, full(s));
+#pragma unroll
+        for (int c = 0; c < T::kColTiles; ++c) {
+          // A last token tile of fewer than 129 rows has no second scale
+          // tile; the first is loaded again for columns that are not stored.
+          int xt = m0 / 128 + c;
+          if (xt >= x_tiles) xt = x_tiles - 1;
+          bulk_load(stage(s) + T::kABytes + T::kBBytes + T::kSfaBytes + c * T::kWords * 512,
+                    a.xscales + (static_cast<int64_t>(xt) * words +
+                                 static_cast<int64_t>(kb_begin + kb) * T::kWords) * 512,
+                    w, full(s));
+        }
+      };
+      const int first = num_kb < S ? num_kb : S;
+      if (!static_w) pdl_wait();
+      for (int kb = 0; kb < first; ++kb) load_w(kb);
+      if (static_w) pdl_wait();
+      for (int kb = 0; kb < first; ++kb) load_x(kb);
+      int stop = first;
+      for (int kb = first; kb < num_kb; ++kb) {
+        if (!mbar_wait(empty(kb % S), ((kb / S) & 1u) ^ 1u, abort_flag, err, kKernelIdFp4)) break;
+        load_w(kb);
+        load_x(kb);
+        stop = kb + 1;
+      }
+      if (*abort_flag) {
+        // Drain this CTA's own loads before leaving.
+        for (int kb = stop - S; kb < stop; ++kb) {
+          if (kb < 0) continue;
+          volatile int dummy = 0;
+          mbar_wait(full(kb % S), (kb / S) & 1u, &dummy, err, kKernelIdFp4, kWaitLimitNs / 4);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA --
+    if (lane == 0) {
+      bool issued = false;
+      for (int kb = 0; kb < num_kb; ++kb) {
+        const int s = kb % S;
+        if (!mbar_wait(full(s), (kb / S) & 1u, abort_flag, err, kKernelIdFp4)) break;
+        tc_fence_after();
+        const int left = a.K - (kb_begin + kb) * kStageK;
+        const int steps = left < kStageK ? left / 64 : kStageK / 64;
+        const int w_here = steps * T::kWords / 4;
+        const uint32_t sfa = tmem + NB + (kb & 1) * T::kSfCols;
+        const uint32_t sfb = sfa + 4 * T::kWords;
+        const uint32_t sf_smem = stage(s) + T::kABytes + T::kBBytes;
+#pragma unroll
+        for (int w = 0; w < T::kWords; ++w) {
+          if (w >= w_here) break;
+          tmem_cp_scales(sfa + 4 * w, sf_smem + 512 * w);
+#pragma unroll
+          for (int c = 0; c < T::kColTiles; ++c)
+            tmem_cp_scales(sfb + 4 * (w * T::kColTiles + c),
+                           sf_smem + T::kSfaBytes + 512 * (c * T::kWords + w));
+        }
+        const uint64_t da = sdesc_k_sw128(stage(s));
+        const uint64_t db = sdesc_k_sw128(stage(s) + T::kABytes);
+#pragma unroll
+        for (int kk = 0; kk < kStageK / 64; ++kk) {
+          if (kk >= steps) break;
+          // 64 channels are 32 bytes (+2 in the address field); an mx scale
+          // word holds two such steps, an nv word one.
+          const int w = FMT == kFp4Mx ? kk / 2 : kk;
+          const int id = FMT == kFp4Mx ? (kk & 1) * 2 : 0;
+          umma_fp4<FMT>(tmem, da + 2ull * kk, db + 2ull * kk, idesc_fp4<FMT>(NB, id), sfa + 4 * w,
+                        sfb + 4 * w * T::kColTiles, (kb | kk) != 0);
+        }
+        issued = true;
+        umma_commit(empty(s));
+      }
+      if (!*abort_flag) {
+        umma_commit(acc_full);
+      } else if (issued) {
+        umma_commit(done_bar);  // in-flight MMAs end before TMEM is freed
+        volatile int dummy = 0;
+        mbar_wait(done_bar, 0, &dummy, err, kKernelIdFp4, kWaitLimitNs / 4);
+      }
+    }
+  } else {
+    // ------------------------------------------------------- epilogue --
+    const int q = warp & 3;  // TMEM lane quarter of this warp
+    const int n = n0 + 32 * q + lane;
+    pdl_wait();
+    const float wr = (a.wrow && n < a.N) ? __ldg(a.wrow + n) : 1.f;
+    const bool ok = mbar_wait(acc_full, 0, abort_flag, err, kKernelIdFp4);
+    tc_fence_after();
+    if (ok) {
+      const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
+      if (ks > 1) {
+        // fp32 partial tile [token][channel] into the idle stage buffers.
+        float* part = reinterpret_cast<float*>(base_ptr);
+#pragma unroll 1
+        for (int c = 0; c < NB; c += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(lane_addr + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            part[(c + i) * kRows + 32 * q + lane] = __uint_as_float(r[i]);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < NB; c += 16) {
+          if (m0 + c >= a.M) break;
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(lane_addr + c, r);
+          tmem_ld_wait();
+          if (n < a.N) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int m = m0 + c + i;
+              if (m < a.M) {
+                const float xr = a.xrow ? __ldg(a.xrow + m) : 1.f;
+                a.y[static_cast<int64_t>(m) * a.N + n] =
+                    __float2bfloat16_rn(__uint_as_float(r[i]) * wr * xr);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  if (ks > 1) {
+    // Every thread of every CTA of the cluster passes both barriers, also
+    // after a timeout, so none is left waiting.
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();  // all partial tiles written
+    if (warp >= 2 && !*abort_flag) {
+      // CTA `rank` adds its share of the tile (pieces of 4 channels of a
+      // token) over the cluster in rank order.
+      const int live = a.M - m0 < NB ? a.M - m0 : NB;
+      const int total = live * (kRows / 4);
+      const int e1 = static_cast<int>(static_cast<int64_t>(rank + 1) * total / ks);
+      float* part = reinterpret_cast<float*>(base_ptr);
+      for (int e = static_cast<int>(static_cast<int64_t>(rank) * total / ks) + threadIdx.x - 64;
+           e < e1; e += kFp4Threads - 64) {
+        const int off = 4 * e;
+        float4 t[kMaxSplit];
+#pragma unroll
+        for (int p = 0; p < kMaxSplit; ++p)
+          if (p < ks) t[p] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, p) + off);
+        float v[4] = {t[0].x, t[0].y, t[0].z, t[0].w};
+#pragma unroll
+        for (int p = 1; p < kMaxSplit; ++p)
+          if (p < ks) {
+            v[0] += t[p].x;
+            v[1] += t[p].y;
+            v[2] += t[p].z;
+            v[3] += t[p].w;
+          }
+        const int m = m0 + off / kRows, n = n0 + off % kRows;
+        const float xr = a.xrow ? __ldg(a.xrow + m) : 1.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (a.wrow && n + i < a.N) v[i] *= __ldg(a.wrow + n + i);
+        __nv_bfloat16* dst = a.y + static_cast<int64_t>(m) * a.N + n;
+        if (n + 4 <= a.N && (a.N & 3) == 0) {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0] * xr, v[1] * xr);
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(v[2] * xr, v[3] * xr);
+          *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                      *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+          for (int i = 0; i < 4; ++i)
+            if (n + i < a.N) dst[i] = __float2bfloat16_rn(v[i] * xr);
+        }
+      }
+    }
+    cluster.sync();  // peers keep their partials until every reader is done
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, T::kTmemCols);
+  }
+}
+
+CUresult encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int box_rows) {
+  static PFN_cuTensorMapEncodeTiled fn = nullptr;
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !p)
+      return CUDA_ERROR_NOT_FOUND;
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled>(p);
+  }
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+  const cuuint32_t box[2] = {kStageK / 2, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+template <auto kern, size_t kBytes>
+cudaError_t opt_in_smem() {
+  static unsigned long long done = 0;  // bit d: device d
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kBytes));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  return cudaSuccess;
+}
+
+template <int FMT, int NB>
+cudaError_t launch(const uint8_t* xcodes, const uint8_t* wcodes, Fp4Args a, int static_w,
+                   cudaStream_t stream, int num_sms, unsigned* err) {
+  using T = Fp4Tile<FMT, NB>;
+  constexpr auto kern = fp4_gemm_kernel<FMT, NB>;
+  CUtensorMap tw, tx;
+  if (encode_codes(&tw, wcodes, a.N, a.K, kRows) != CUDA_SUCCESS ||
+      encode_codes(&tx, xcodes, a.M, a.K, NB) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  cudaError_t e = opt_in_smem<kern, T::bytes>();
+  if (e != cudaSuccess) return e;
+  a.m_tiles = (a.M + NB - 1) / NB;
+  const int64_t tiles = static_cast<int64_t>((a.N + kRows - 1) / kRows) * a.m_tiles;
+  const int num_kb = (a.K + kStageK - 1) / kStageK;
+  // K is split while the CTAs still fit the GPU at once.
+  int ks = 1;
+  const int64_t slots = static_cast<int64_t>(num_sms) * T::kCtasPerSm;
+  while (ks < kMaxSplit && ks < num_kb && tiles * (ks + 1) <= slots) ++ks;
+  static_assert(NB * kRows * 4 <= T::kStages * T::kStageBytes, "a partial tile fits the stages");
+  if (tiles * ks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ks), 1, 1);
+  cfg.blockDim = dim3(kFp4Threads, 1, 1);
+  cfg.dynamicSmemBytes = T::bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, tw, tx, a, static_w, err);
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const uint8_t* xcodes, const uint8_t* wcodes, const Fp4Args& a,
+                       int static_w, cudaStream_t s, int sms, unsigned* err) {
+  if (a.M <= 16) return launch<FMT, 16>(xcodes, wcodes, a, static_w, s, sms, err);
+  if (a.M <= 32) return launch<FMT, 32>(xcodes, wcodes, a, static_w, s, sms, err);
+  if (a.M <= 64) return launch<FMT, 64>(xcodes, wcodes, a, static_w, s, sms, err);
+  if (a.M <= 128) return launch<FMT, 128>(xcodes, wcodes, a, static_w, s, sms, err);
+  return launch<FMT, 256>(xcodes, wcodes, a, static_w, s, sms, err);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_linear(const uint8_t* xcodes, const uint8_t* xscales, const float* xrow,
+                              int M, const uint8_t* wcodes, const uint8_t* wscales,
+                              const float* wrow, int N, int K, int fmt, void* y, bool static_w,
+                              cudaStream_t stream, int num_sms, unsigned* err) {
+  Fp4Args a;
+  a.wscales = wscales;
+  a.xscales = xscales;
+  a.wrow = wrow;
+  a.xrow = xrow;
+  a.y = static_cast<__nv_bfloat16*>(y);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.m_tiles = 1;
+  return fmt == kFp4Mx ? launch_fmt<kFp4Mx>(xcodes, wcodes, a, static_w, stream, num_sms, err)
+                       : launch_fmt<kFp4Nv>(xcodes, wcodes, a, static_w, stream, num_sms, err);
+}
+
+}  // namespace w4

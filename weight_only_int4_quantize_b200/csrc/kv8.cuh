@@ -1,0 +1,59 @@
+// Shared definitions of the 8-bit paged KV cache kernels.
+//
+// Layout: keys [page][kv head][token in page][channel], values
+// [page][kv head][channel][token in page], one byte each (int8 or e4m3), and
+// one fp32 scale for each page and kv head of either side.  With both sides
+// contiguous along the axis that their product sums over, 16 bytes of a key
+// row (channels) and 16 bytes of a value row (tokens) are each an operand
+// fragment that a lane can use as loaded.
+#pragma once
+
+#include "w4_common.cuh"
+
+namespace w4 {
+
+enum : int { kKvInt8 = 0, kKvE4m3 = 1 };
+
+// Device error word, bit 1: a page id, a length or a row offset outside the
+// caller's buffers was met; what it addressed was skipped.
+constexpr unsigned kErrBadIndex = 2u;
+
+__host__ __device__ constexpr float kv8_qmax(int fmt) { return fmt == kKvInt8 ? 127.f : 448.f; }
+
+struct Kv8Cache {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  int num_pages, heads, log_page;
+};
+
+struct Kv8Batch {
+  const int32_t* table;   // [batch, max_pages]
+  const int32_t* lens;    // [batch] tokens in the cache, the new ones included
+  const int32_t* starts;  // [batch + 1] rows of the new tokens; NULL: row b alone
+  int batch, max_pages, rows;  // rows: of the q / k / v buffers
+  int max_new;
+};
+
+// One sequence's length, new tokens and first row, checked against the
+// buffers: anything outside them counts as no new tokens.
+struct Kv8Seq {
+  int len, n, row0;
+  bool bad;
+};
+
+__device__ __forceinline__ Kv8Seq kv8_sequence(const Kv8Batch& p, int b, int log_page) {
+  Kv8Seq s;
+  s.len = p.lens[b];
+  s.row0 = p.starts ? p.starts[b] : b;
+  const int end = p.starts ? p.starts[b + 1] : b + 1;
+  const int64_t room = static_cast<int64_t>(p.max_pages) << log_page;
+  s.bad = s.len < 0 || s.len > room || s.row0 < 0 || end < s.row0 || end > p.rows ||
+          static_cast<int64_t>(end) - s.row0 > p.max_new;
+  s.n = s.bad ? 0 : end - s.row0;
+  if (s.bad) s.len = 0;
+  return s;
+}
+
+}  // namespace w4

@@ -228,6 +228,27 @@ cudaError_t block_search(const BlockConfig* c, const double* x, int64_t T, const
                          const float* shrinks, int n_shrink, bool sym, int32_t* choice,
                          double* losses, void* workspace, cudaStream_t st, unsigned* err);
 
+// Microscaled 4-bit floating point (fp4_quant.cu, fp4_gemm.cu; formats and
+// layouts in fp4.cuh).  ldx: row stride of x in elements; values may be NULL.
+cudaError_t launch_fp4_quantize(const void* x, int64_t R, int64_t K, int64_t ldx, int fmt,
+                                uint8_t* codes, uint8_t* scales, float* row_scale, void* values,
+                                cudaStream_t stream, int num_sms);
+cudaError_t launch_fp4_linear(const uint8_t* xcodes, const uint8_t* xscales, const float* xrow,
+                              int M, const uint8_t* wcodes, const uint8_t* wscales,
+                              const float* wrow, int N, int K, int fmt, void* y, bool static_w,
+                              cudaStream_t stream, int num_sms, unsigned* err);
+
+// 8-bit paged KV cache (kv8_append.cu, kv8_attn.cu; layout in kv8.cuh).  ldk,
+// ldv, ldq: elements between the tokens of k, v and q.
+struct Kv8Cache;
+struct Kv8Batch;
+cudaError_t launch_kv8_append(const Kv8Cache& c, const Kv8Batch& bt, const void* k, const void* v,
+                              int64_t ldk, int64_t ldv, int D, int fmt, cudaStream_t stream,
+                              unsigned* err);
+cudaError_t launch_kv8_attention(const Kv8Cache& c, const Kv8Batch& bt, const void* q, int64_t ldq,
+                                 int q_heads, int D, int fmt, float scale, void* out,
+                                 cudaStream_t stream, int num_sms, unsigned* err);
+
 // Device address of the fixed scratch behind awq_score_grid_static_scratch
 // on the current device (looked up once per device, then cached).
 cudaError_t awq_static_scratch_address(void** ptr);
