@@ -187,7 +187,7 @@ def _cuda(t, dtype, name):
 def _expect(t, shape, name):
     """Shape check of a companion tensor: the C ABI takes bare pointers and
     cannot see a mis-sized buffer, so the binding refuses it here."""
-    if t is not None and tuple(t.shape) != tuple(int(v) for v in shape):
+    if t is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -683,9 +683,10 @@ FP4_FORMATS = {"mx": (0, 32), "nv": (1, 16)}
 
 
 def _fp4_format(fmt):
-    if fmt not in FP4_FORMATS:
+    f = FP4_FORMATS.get(fmt)
+    if f is None:
         raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {fmt!r}")
-    return FP4_FORMATS[fmt]
+    return f
 
 
 def fp4_scale_shape(rows: int, k: int, fmt: str):
@@ -694,9 +695,35 @@ def fp4_scale_shape(rows: int, k: int, fmt: str):
     return ((rows + 127) // 128, k // (4 * block), 512)
 
 
+# The operators below are called once per linear or layer of a decode step, so
+# the binding's own time counts: it asks torch for plain integers (device
+# index, raw stream) and enters a device context only where the tensors' is
+# not the current one.
+
+
+def _call(fn, where, index, args):
+    """fn(*args, current stream of device `index`) with that device current."""
+    torch = _torch()
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, stream)
+    if st != 0:
+        raise W4Error(st, where)
+
+
+def _on_device(t, index, name):
+    if t is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{index}")
+
+
 def _rows_of(t, width, name):
     """Elements between the rows of a tensor whose rows (everything but the
     first axis) are contiguous: slices of a wider buffer's rows are allowed."""
+    if t.is_contiguous():
+        return width
     inner = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and stride != inner:
@@ -730,15 +757,13 @@ def fp4_quantize(x, fmt: str = "mx", values: bool = False):
         raise ValueError("x must be [R, K]")
     r, k = x.shape
     ldx = _rows_of(x, k, "x")
-    codes = torch.empty((r, k // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(fp4_scale_shape(r, k, fmt), dtype=torch.uint8, device=x.device)
-    row = torch.empty((r,), dtype=torch.float32, device=x.device) if fmt == "nv" else None
-    val = torch.empty((r, k), dtype=torch.bfloat16, device=x.device) if values else None
-    with torch.cuda.device(x.device):
-        st = lib().w4_fp4_quantize(x.data_ptr(), r, k, ldx, f, codes.data_ptr(),
-                                   scales.data_ptr(), None if row is None else row.data_ptr(),
-                                   None if val is None else val.data_ptr(), _stream(x.device))
-    _check(st, "w4_fp4_quantize")
+    codes = x.new_empty((r, k // 2), dtype=torch.uint8)
+    scales = x.new_empty(((r + 127) // 128, k // (4 * block), 512), dtype=torch.uint8)
+    row = x.new_empty((r,), dtype=torch.float32) if f == 1 else None
+    val = x.new_empty((r, k)) if values else None
+    _call(lib().w4_fp4_quantize, "w4_fp4_quantize", x.get_device(),
+          (x.data_ptr(), r, k, ldx, f, codes.data_ptr(), scales.data_ptr(),
+           None if row is None else row.data_ptr(), None if val is None else val.data_ptr()))
     return (codes, scales, row, val) if values else (codes, scales, row)
 
 
@@ -747,35 +772,38 @@ def fp4_linear(xcodes, xscales, xrow, wcodes, wscales, wrow, fmt: str = "mx", fl
     """y = x . w^T, bf16 [M, N], of an activation and a weight in the same
     microscaled 4-bit format (each as fp4_quantize returns it)."""
     torch = _torch()
-    f, _ = _fp4_format(fmt)
-    for t, name in ((xcodes, "xcodes"), (xscales, "xscales"), (wcodes, "wcodes"),
-                    (wscales, "wscales")):
-        _cuda(t, torch.uint8, name)
+    f, block = _fp4_format(fmt)
+    u8 = torch.uint8
+    _cuda(xcodes, u8, "xcodes")
+    _cuda(xscales, u8, "xscales")
+    _cuda(wcodes, u8, "wcodes")
+    _cuda(wscales, u8, "wscales")
     if xcodes.dim() != 2 or wcodes.dim() != 2:
         raise ValueError("xcodes and wcodes must be [rows, K/2]")
-    m, k = xcodes.shape[0], xcodes.shape[1] * 2
-    n = wcodes.shape[0]
-    _expect(wcodes, (n, k // 2), "wcodes")
-    _expect(xscales, fp4_scale_shape(m, k, fmt), "xscales")
-    _expect(wscales, fp4_scale_shape(n, k, fmt), "wscales")
-    for t, rows, name in ((xrow, m, "xrow"), (wrow, n, "wrow")):
-        if (t is None) != (fmt == "mx"):
-            raise ValueError(f"{name} belongs to format 'nv' alone")
-        if t is not None:
-            _cuda(t, torch.float32, name)
-            _expect(t, (rows,), name)
+    m, k2 = xcodes.shape
+    k, n, tiles = 2 * k2, wcodes.shape[0], 2 * k2 // (4 * block)
+    _expect(wcodes, (n, k2), "wcodes")
+    _expect(xscales, ((m + 127) // 128, tiles, 512), "xscales")
+    _expect(wscales, ((n + 127) // 128, tiles, 512), "wscales")
+    if (xrow is None) != (f == 0) or (wrow is None) != (f == 0):
+        raise ValueError("xrow and wrow belong to format 'nv' alone")
+    if f == 1:
+        _cuda(xrow, torch.float32, "xrow")
+        _cuda(wrow, torch.float32, "wrow")
+        _expect(xrow, (m,), "xrow")
+        _expect(wrow, (n,), "wrow")
     if out is not None:
         _cuda(out, torch.bfloat16, "out")
         _expect(out, (m, n), "out")
-    _same_device(xcodes, xscales=xscales, xrow=xrow, wcodes=wcodes, wscales=wscales, wrow=wrow,
-                 out=out)
-    y = out if out is not None else torch.empty((m, n), dtype=torch.bfloat16, device=xcodes.device)
-    with torch.cuda.device(xcodes.device):
-        st = lib().w4_fp4_linear(xcodes.data_ptr(), xscales.data_ptr(),
-                                 None if xrow is None else xrow.data_ptr(), m, wcodes.data_ptr(),
-                                 wscales.data_ptr(), None if wrow is None else wrow.data_ptr(), n,
-                                 k, f, y.data_ptr(), int(flags), _stream(xcodes.device))
-    _check(st, "w4_fp4_linear")
+    at = xcodes.get_device()
+    for t, name in ((xscales, "xscales"), (wcodes, "wcodes"), (wscales, "wscales"),
+                    (xrow, "xrow"), (wrow, "wrow"), (out, "out")):
+        _on_device(t, at, name)
+    y = out if out is not None else xcodes.new_empty((m, n), dtype=torch.bfloat16)
+    _call(lib().w4_fp4_linear, "w4_fp4_linear", at,
+          (xcodes.data_ptr(), xscales.data_ptr(), None if xrow is None else xrow.data_ptr(), m,
+           wcodes.data_ptr(), wscales.data_ptr(), None if wrow is None else wrow.data_ptr(), n, k,
+           f, y.data_ptr(), int(flags)))
     return y
 
 
@@ -807,28 +835,30 @@ def kv8_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, dtyp
         raise TypeError("cache codes are int8 or float8_e4m3fn")
     k = torch.zeros((num_pages, kv_heads, page_size, head_dim), dtype=torch.uint8, device=device)
     v = torch.zeros((num_pages, kv_heads, head_dim, page_size), dtype=torch.uint8, device=device)
-    s = torch.zeros((2, num_pages, kv_heads), dtype=torch.float32, device=device)
-    return KV8Cache(k.view(dtype), v.view(dtype), s[0].clone(), s[1].clone())
+    s = [torch.zeros((num_pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return KV8Cache(k.view(dtype), v.view(dtype), *s)
 
 
 def _kv8_args(ref, cache, page_table, seq_lens, starts, max_new):
     """Checks of what appending and attention share; ref is [rows, heads,
     head_dim].  Returns the C cache, the batch size and max_new."""
     torch = _torch()
-    k = cache.k_codes
+    k, v, ks, vs = cache
     if not isinstance(k, torch.Tensor) or k.dtype not in (torch.int8, torch.float8_e4m3fn):
         raise TypeError("cache codes must be int8 or float8_e4m3fn")
-    _cuda(k, k.dtype, "k_codes")
-    _cuda(cache.v_codes, k.dtype, "v_codes")
+    dt = k.dtype
+    _cuda(k, dt, "k_codes")
+    _cuda(v, dt, "v_codes")
+    _cuda(ks, torch.float32, "k_scales")
+    _cuda(vs, torch.float32, "v_scales")
+    _cuda(page_table, torch.int32, "page_table")
+    _cuda(seq_lens, torch.int32, "seq_lens")
     if k.dim() != 4:
         raise ValueError("k_codes must be [pages, kv_heads, page_size, head_dim]")
     pages, heads, page, d = k.shape
-    _expect(cache.v_codes, (pages, heads, d, page), "v_codes")
-    for t, name in ((cache.k_scales, "k_scales"), (cache.v_scales, "v_scales")):
-        _cuda(t, torch.float32, name)
-        _expect(t, (pages, heads), name)
-    _cuda(page_table, torch.int32, "page_table")
-    _cuda(seq_lens, torch.int32, "seq_lens")
+    _expect(v, (pages, heads, d, page), "v_codes")
+    _expect(ks, (pages, heads), "k_scales")
+    _expect(vs, (pages, heads), "v_scales")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [batch, max_pages]")
     b = page_table.shape[0]
@@ -842,11 +872,12 @@ def _kv8_args(ref, cache, page_table, seq_lens, starts, max_new):
         raise ValueError("without starts every sequence has one new token")
     if ref.dim() != 3 or ref.shape[2] != d:
         raise ValueError(f"new tokens must be [rows, heads, {d}]")
-    _same_device(ref, k_codes=k, v_codes=cache.v_codes, k_scales=cache.k_scales,
-                 v_scales=cache.v_scales, page_table=page_table, seq_lens=seq_lens, starts=starts)
-    c = _KV8Cache(k.data_ptr(), cache.v_codes.data_ptr(), cache.k_scales.data_ptr(),
-                  cache.v_scales.data_ptr(), pages, heads, page, d,
-                  0 if k.dtype == torch.int8 else 1)
+    at = ref.get_device()
+    for t, name in ((k, "k_codes"), (v, "v_codes"), (ks, "k_scales"), (vs, "v_scales"),
+                    (page_table, "page_table"), (seq_lens, "seq_lens"), (starts, "starts")):
+        _on_device(t, at, name)
+    c = _KV8Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, heads, page, d,
+                  0 if dt == torch.int8 else 1)
     return c, b, 1 if max_new is None else int(max_new)
 
 
@@ -859,17 +890,17 @@ def kv8_append(cache, k, v, page_table, seq_lens, starts=None, max_new=None) -> 
     _cuda_rows(k, torch.bfloat16, "k")
     _cuda_rows(v, torch.bfloat16, "v")
     c, b, most = _kv8_args(k, cache, page_table, seq_lens, starts, max_new)
-    _expect(k, (k.shape[0], c.kv_heads, c.head_dim), "k")
-    _expect(v, tuple(k.shape), "v")
-    _same_device(k, v=v)
-    width = c.kv_heads * c.head_dim
-    ldk, ldv = _rows_of(k, width, "k"), _rows_of(v, width, "v")
-    with torch.cuda.device(k.device):
-        st = lib().w4_kv8_append(ctypes.byref(c), k.data_ptr(), ldk, v.data_ptr(), ldv, k.shape[0],
-                                 page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
-                                 None if starts is None else starts.data_ptr(), b, most,
-                                 _stream(k.device))
-    _check(st, "w4_kv8_append")
+    rows, heads, d = k.shape
+    if heads != c.kv_heads:
+        raise ValueError(f"k has {heads} heads, the cache {c.kv_heads}")
+    _expect(v, (rows, heads, d), "v")
+    at = k.get_device()
+    _on_device(v, at, "v")
+    ldk, ldv = _rows_of(k, heads * d, "k"), _rows_of(v, heads * d, "v")
+    _call(lib().w4_kv8_append, "w4_kv8_append", at,
+          (ctypes.byref(c), k.data_ptr(), ldk, v.data_ptr(), ldv, rows, page_table.data_ptr(),
+           page_table.shape[1], seq_lens.data_ptr(), None if starts is None else starts.data_ptr(),
+           b, most))
 
 
 def kv8_attention(q, cache, page_table, seq_lens, starts=None, max_new=None, scale=None, out=None):
@@ -883,20 +914,16 @@ def kv8_attention(q, cache, page_table, seq_lens, starts=None, max_new=None, sca
     c, b, most = _kv8_args(q, cache, page_table, seq_lens, starts, max_new)
     rows, heads, d = q.shape
     ldq = _rows_of(q, heads * d, "q")
+    at = q.get_device()
     if out is not None:
         _cuda(out, torch.bfloat16, "out")
         _expect(out, (rows, heads, d), "out")
-        _same_device(q, out=out)
-    o = out if out is not None else torch.empty((rows, heads, d), dtype=torch.bfloat16,
-                                                device=q.device)
-    with torch.cuda.device(q.device):
-        st = lib().w4_kv8_attention(q.data_ptr(), ldq, rows, heads, ctypes.byref(c),
-                                    page_table.data_ptr(), page_table.shape[1],
-                                    seq_lens.data_ptr(),
-                                    None if starts is None else starts.data_ptr(), b, most,
-                                    float(d ** -0.5 if scale is None else scale), o.data_ptr(),
-                                    _stream(q.device))
-    _check(st, "w4_kv8_attention")
+        _on_device(out, at, "out")
+    o = out if out is not None else q.new_empty((rows, heads, d))
+    _call(lib().w4_kv8_attention, "w4_kv8_attention", at,
+          (q.data_ptr(), ldq, rows, heads, ctypes.byref(c), page_table.data_ptr(),
+           page_table.shape[1], seq_lens.data_ptr(), None if starts is None else starts.data_ptr(),
+           b, most, float(d ** -0.5 if scale is None else scale), o.data_ptr()))
     return o
 
 
