@@ -6,29 +6,32 @@
 //
 // Rows: the query heads that share a kv head and the new tokens of a
 // sequence are the rows of one problem (row = token * group + head of the
-// group), taken 16 at a time as the M of mma.m16n8k16.  The cache is read
-// once per 16 rows, so for single tokens the kernel is bound by HBM.
+// group), taken 8 or 16 at a time (NT = 1, 2) as the N of mma.m16n8k16: the
+// products are S^T = K Q^T and O^T = V^T P^T, so the cache is the A operand
+// and no multiply is spent on rows that a small group does not have.
 //
 // Work split: a thread-block cluster of `ks` CTAs owns one (sequence, kv
-// head, 16 rows); its warps take tiles of 64 tokens in turn.  Each warp runs
+// head, row tile); its warps take tiles of 64 tokens in turn.  Each warp runs
 // its own online softmax; the partial results are joined in a fixed order,
 // first over a CTA's warps and then, through distributed shared memory, over
 // the cluster: no workspace, and the same bits on every run.
 //
 // A warp streams its tiles through its own ring of shared memory: each lane
-// copies (cp.async, 16 bytes) exactly the bytes of its own operand
-// fragments and reads only those back, so the ring needs no barrier.
-//   keys:   the columns of score tile j (8 tokens) are the tokens
-//           16 (c / 2) + 2 j + c % 2, and k-step s of a lane quad covers
-//           channels 64 (s / 4) + 16 t + 4 (s % 4) + 0..3 (the queries are
-//           loaded in that order), so a lane's fragments are 16 contiguous
-//           bytes of a key row;
-//   values: with that order of columns the probabilities that a lane holds
-//           after the score product are its A fragments for the tokens
-//           16 t .. 16 t + 15, so its value fragments are 16 contiguous bytes
-//           of a value row.
-// Each lane's 16 score columns lie in one page whatever the page size (>= 16),
-// so a key scale and a value scale per lane and tile suffice.
+// (g = lane / 4, t = lane % 4) copies (cp.async, 16 bytes) exactly the bytes
+// of its own operand fragments and reads only those back, so the ring needs
+// no barrier.
+//   keys:   row r of score tile i (16 tokens) is token 16 (r / 2) + 4 i + r % 2
+//           of the 64, rows r >= 8 token 16 (r / 2 - 4) + 4 i + 2 + r % 2, and
+//           k-step s covers channels 64 (s / 4) + 16 t + 4 (s % 4) + 0..3 of
+//           lane quad t (the queries are loaded in that order), so a lane's
+//           fragments are 16 contiguous bytes of key rows;
+//   values: the probabilities of score tile i, transposed 8 x 8 at a time
+//           (movmatrix), are the B fragments of k-step i; with that order of
+//           rows a lane's value fragments are the tokens 16 t .. 16 t + 15,
+//           16 contiguous bytes of a value row.
+// A lane's score rows all lie in the 16 tokens of granule g / 2, so in one
+// page whatever the page size (>= 16): a key scale and a value scale per lane
+// and tile suffice.
 //
 // Numerics: codes are exact in fp16.  Each query row is scaled by a power of
 // two that brings its largest magnitude into [128, 256) (exact for channels
@@ -115,13 +118,23 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   }
 }
 
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+// Transposes an 8 x 8 matrix of 16-bit values held two per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
-__device__ __forceinline__ float quad_sum(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+
+// Over the eight lanes of one t (the rows of a score tile).
+__device__ __forceinline__ float column_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
 }
 
 struct AttnArgs {
@@ -134,13 +147,14 @@ struct AttnArgs {
   float scale_log2;  // softmax scale * log2(e)
 };
 
-template <int FMT, int D>
+template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads, 2)
     kv8_attention_rows_kernel(const AttnArgs a, unsigned* err) {
   using SM = AttnSmem<D>;
-  constexpr int kSteps = D / 16;       // k-steps of the score product
-  constexpr int kChunks = D / 64;      // 16-byte pieces of a key row per lane
-  constexpr int kDTiles = D / 8;       // 8-channel tiles of the output
+  constexpr int kRows = 8 * NT;
+  constexpr int kSteps = D / 16;    // k-steps of the score product
+  constexpr int kChunks = D / 64;   // 16-byte pieces of a key row per lane
+  constexpr int kDTiles = D / 16;   // 16-channel tiles of the output
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -157,54 +171,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   if (s.bad && threadIdx.x == 0 && h == 0 && rt == 0 && rank == 0)
     record_error(err, kErrBadIndex, kKernelIdAttn);
   const int n_rows = s.n * a.group;
-  const int r0 = rt * 16;
+  const int r0 = rt * kRows;
   if (r0 >= n_rows) return;  // the whole cluster
-  const int live_rows = n_rows - r0 < 16 ? n_rows - r0 : 16;
-
-  // Rows g and g + 8 of this lane: the last position each sees.
-  int limit[2];
-  uint32_t qa[kSteps][4];
-  float q_back[2];  // undoes the query scaling, times the softmax scale
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = r0 + g + 8 * i;
-    const bool live = r < n_rows;
-    const int tok = live ? r / a.group : 0;
-    limit[i] = live ? s.len - s.n + tok : -1;
-    const __nv_bfloat16* qr = a.q + static_cast<int64_t>(s.row0 + tok) * a.ldq +
-                              (h * a.group + (live ? r % a.group : 0)) * D;
-    uint32_t raw[kSteps][2];
-    uint32_t big = 0;
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st) {
-      const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(
-                                 qr + 64 * (st / 4) + 16 * t + 4 * (st % 4)))
-                           : make_uint2(0, 0);
-      raw[st][0] = v.x;
-      raw[st][1] = v.y;
-      const uint32_t m = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
-      big = __vmaxu2(big, m);
-    }
-    big = max(big & 0xFFFFu, big >> 16);
-    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-    big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    // Largest magnitude in [2^e, 2^(e+1)); scaled by 2^(7 - e).
-    const int e = static_cast<int>(big >> 7) - 127;
-    const float up = __int_as_float((min(7 - e, 126) + 127) << 23);
-    q_back[i] = __int_as_float((max(e - 7, -126) + 127) << 23) * a.scale_log2;
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st)
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const __half2 x = __floats2half2_rn(__uint_as_float(raw[st][w] << 16) * up,
-                                            __uint_as_float(raw[st][w] & 0xFFFF0000u) * up);
-        qa[st][2 * w + i] = *reinterpret_cast<const uint32_t*>(&x);
-      }
-  }
+  const int live_rows = n_rows - r0 < kRows ? n_rows - r0 : kRows;
 
   // Tiles of this CTA: the cluster's tiles in contiguous shares.
-  const int last_tok = (r0 + live_rows - 1) / a.group;  // the tile's last new token
-  const int keys = s.len - s.n + last_tok + 1;          // <= 0: nothing is seen
+  const int keys = s.len - s.n + (r0 + live_rows - 1) / a.group + 1;  // <= 0: nothing is seen
   const int first_limit = s.len - s.n + r0 / a.group;
   const int tiles = keys > 0 ? (keys + kTileTokens - 1) / kTileTokens : 0;
   const int t_begin = static_cast<int>(static_cast<int64_t>(rank) * tiles / ks);
@@ -238,11 +210,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       const int64_t head = (static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h)
                            << a.c.log_page;
       if (u & 1) {
+        // channels g, g + 8, g + 16, ... of the lane's 16 tokens
         const uint8_t* src = a.c.v + head * D + in_page + (static_cast<int64_t>(g) << a.c.log_page);
 #pragma unroll
-        for (int j = 0; j < kDTiles; ++j)
+        for (int j = 0; j < 2 * kDTiles; ++j)
           cp_async16(dst + j * 512, src + (static_cast<int64_t>(8 * j) << a.c.log_page), page >= 0);
       } else {
+        // tokens g % 2, g % 2 + 2, + 4, ... of granule g / 2
         const uint8_t* src = a.c.k + (head + in_page + (g & 1)) * D + 16 * t;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -253,19 +227,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     }
     cp_commit();
   };
-
-  float o[kDTiles][4];
-#pragma unroll
-  for (int j = 0; j < kDTiles; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float v_ref = 0.f;  // largest value scale so far: o is in its units
-
 #pragma unroll
   for (int u = 0; u < kSlots; ++u) issue(u);
   auto scales_of = [&](int i, float& sk, float& sv) {
-    const int p = page_of(i, t);
+    const int p = page_of(i, g >> 1);
     const int64_t at = static_cast<int64_t>(p < 0 ? 0 : p) * a.c.heads + h;
     sk = p < 0 ? 0.f : __ldg(a.c.ks + at);
     sv = p < 0 ? 0.f : __ldg(a.c.vs + at);
@@ -273,78 +238,151 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   float sk_next, sv_next;
   scales_of(0, sk_next, sv_next);
 
+  // Query fragments: row 8 nt + g, scaled by a power of two.
+  uint32_t qb[NT][kSteps][2];
+  float q_back[NT][2];  // of rows 8 nt + 2 t, + 1: undoes the scaling, times the softmax scale
+  int limit[NT][2];     // the last position that each of these rows sees
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = r0 + 8 * nt + g;
+    const bool live = r < n_rows;
+    const int tok = live ? r / a.group : 0;
+    const __nv_bfloat16* qr = a.q + static_cast<int64_t>(s.row0 + tok) * a.ldq +
+                              (h * a.group + (live ? r - tok * a.group : 0)) * D;
+    uint32_t raw[kSteps][2];
+    uint32_t big = 0;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(
+                                 qr + 64 * (st / 4) + 16 * t + 4 * (st % 4)))
+                           : make_uint2(0, 0);
+      raw[st][0] = v.x;
+      raw[st][1] = v.y;
+      big = __vmaxu2(big, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
+    }
+    big = max(big & 0xFFFFu, big >> 16);
+    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    // Largest magnitude in [2^e, 2^(e+1)); scaled by 2^(7 - e).
+    const int e = static_cast<int>(big >> 7) - 127;
+    const float up = __int_as_float((min(7 - e, 126) + 127) << 23);
+    const float back = __int_as_float((max(e - 7, -126) + 127) << 23) * a.scale_log2;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const __half2 x = __floats2half2_rn(__uint_as_float(raw[st][w] << 16) * up,
+                                            __uint_as_float(raw[st][w] & 0xFFFF0000u) * up);
+        qb[nt][st][w] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    const int lim = live ? s.len - s.n + tok : -1;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {  // row 2 t + x lies with the lanes g = 2 t + x
+      q_back[nt][x] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + x));
+      limit[nt][x] = __shfl_sync(0xffffffffu, lim, 4 * (2 * t + x));
+    }
+  }
+
+  float o[NT][kDTiles][4];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int j = 0; j < kDTiles; ++j)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[nt][j][x] = 0.f;
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+  float v_ref = 0.f;  // largest value scale so far: o is in its units
+
   for (int i = 0; i < my_tiles; ++i) {
     const int tok0 = (t_begin + warp + i * kWarps) * kTileTokens;
     const float sk = sk_next, sv = sv_next;
     scales_of(i + 1, sk_next, sv_next);
-    // ---- scores ----
+    // ---- scores: sc[nt][i4][x], tokens 16 (g/2) + 4 i4 + g%2 (+ 2 for x >= 2)
+    // of rows 2 t + x % 2 ----
     cp_wait<kSlots - 1>();
-    float sc[8][4];
+    float sc[NT][4][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sc[nt][j][x] = 0.f;
     {
       const uint32_t src = ring + ((2 * i) % kSlots) * SM::kSlotBytes;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t kw[8][4];  // the lane's eight tokens
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sc[j][x] = 0.f;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
+        for (int j = 0; j < 8; ++j) {
           const uint4 w = lds128(src + (j * kChunks + c) * 512);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t b0, b1;
-            codes_to_f16<FMT>(ww[x], b0, b1);
-            mma_f16(sc[j], qa[4 * c + x], b0, b1);
-          }
+          kw[j][0] = w.x, kw[j][1] = w.y, kw[j][2] = w.z, kw[j][3] = w.w;
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t f[4];
+            codes_to_f16<FMT>(kw[2 * j][x], f[0], f[2]);
+            codes_to_f16<FMT>(kw[2 * j + 1][x], f[1], f[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(sc[nt][j], f, qb[nt][4 * c + x][0], qb[nt][4 * c + x][1]);
+          }
       }
     }
     issue(2 * i + kSlots);
     // ---- online softmax ----
-    const float f[2] = {q_back[0] * sk, q_back[1] * sk};
-    const bool all_seen = tok0 + kTileTokens - 1 <= first_limit && live_rows == 16;
-    float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        float v = sc[j][x] * f[x >> 1];
-        // Columns of this lane: tokens 16 t + 2 j + 0, 1.  A masked column
-        // may hold anything, so it is replaced, not added to.
-        if (!all_seen && tok0 + 16 * t + 2 * j + (x & 1) > limit[x >> 1]) v = -INFINITY;
-        sc[j][x] = v;
-        top[x >> 1] = fmaxf(top[x >> 1], v);
-      }
-    float keep[2];
-    float v_new = fmaxf(v_ref, quad_max(sv));
+    const bool all_seen = tok0 + kTileTokens - 1 <= first_limit;
+    float v_new = fmaxf(v_ref, column_max(sv));
     const float v_old = v_new > 0.f ? v_ref / v_new : 0.f;
     const float v_rel = v_new > 0.f ? sv / v_new : 0.f;
     v_ref = v_new;
-    float base[2];
+    uint32_t pb[NT][4][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float mn = fmaxf(m[r], quad_max(top[r]));
-      const float at = mn == -INFINITY ? 0.f : mn;
-      keep[r] = exp2f(m[r] - at);
-      m[r] = mn;
-      base[r] = at - kShift;
-      l[r] *= keep[r];
-      keep[r] *= v_old;
-    }
-    uint32_t pa[4][4];
+    for (int nt = 0; nt < NT; ++nt) {
+      float keep[2], base[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+      for (int x = 0; x < 2; ++x) {
+        const float f = q_back[nt][x] * sk;
+        const int seen = limit[nt][x] - (tok0 + 16 * (g >> 1) + (g & 1));
+        float top = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float p0 = exp2f(sc[j][2 * r] - base[r]), p1 = exp2f(sc[j][2 * r + 1] - base[r]);
-        l[r] += p0 + p1;
-        const __half2 p = __floats2half2_rn(p0 * v_rel, p1 * v_rel);
-        pa[j >> 1][2 * (j & 1) + r] = *reinterpret_cast<const uint32_t*>(&p);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            float v = sc[nt][j][2 * hi + x] * f;
+            // A masked score may be anything, so it is replaced, not added to.
+            if (!all_seen && 4 * j + 2 * hi > seen) v = -INFINITY;
+            sc[nt][j][2 * hi + x] = v;
+            top = fmaxf(top, v);
+          }
+        const float mn = fmaxf(m[nt][x], column_max(top));
+        const float at = mn == -INFINITY ? 0.f : mn;
+        keep[x] = exp2f(m[nt][x] - at);
+        m[nt][x] = mn;
+        base[x] = at - kShift;
+        l[nt][x] *= keep[x];
+        keep[x] *= v_old;
       }
 #pragma unroll
-    for (int j = 0; j < kDTiles; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) o[j][x] *= keep[x >> 1];
+        for (int hi = 0; hi < 2; ++hi) {
+          const float p0 = exp2f(sc[nt][j][2 * hi] - base[0]);
+          const float p1 = exp2f(sc[nt][j][2 * hi + 1] - base[1]);
+          l[nt][0] += p0;
+          l[nt][1] += p1;
+          const __half2 p = __floats2half2_rn(p0 * v_rel, p1 * v_rel);
+          pb[nt][j][hi] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p));
+        }
+#pragma unroll
+      for (int j = 0; j < kDTiles; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[nt][j][x] *= keep[x & 1];
+    }
     // ---- outputs ----
     cp_wait<kSlots - 1>();
     {
@@ -353,18 +391,29 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       const int held = keys - tok0 - 16 * t;  // tokens of this lane's 16 that count
       const bool ragged = tok0 + kTileTokens > keys;
 #pragma unroll
-      for (int j = 0; j < kDTiles; ++j) {
-        const uint4 w = lds128(src + j * 512);
-        uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      for (int j0 = 0; j0 < kDTiles; j0 += 4) {
+        uint32_t vw[8][4];  // four output tiles: channels g and g + 8 of each
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 w = lds128(src + (2 * j0 + j) * 512);
+          vw[j][0] = w.x, vw[j][1] = w.y, vw[j][2] = w.z, vw[j][3] = w.w;
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
+          uint32_t mask = 0xFFFFFFFFu;
           if (ragged) {
             const int nb = held - 4 * x;  // bytes of this word that count
-            ww[x] &= nb >= 4 ? 0xFFFFFFFFu : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
+            mask = nb >= 4 ? 0xFFFFFFFFu : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
           }
-          uint32_t b0, b1;
-          codes_to_f16<FMT>(ww[x], b0, b1);
-          mma_f16(o[j], pa[x], b0, b1);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t f[4];
+            codes_to_f16<FMT>(vw[2 * j][x] & mask, f[0], f[2]);
+            codes_to_f16<FMT>(vw[2 * j + 1][x] & mask, f[1], f[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[nt][j0 + j], f, pb[nt][x][0], pb[nt][x][1]);
+          }
         }
       }
     }
@@ -374,22 +423,26 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   if (bad_page) record_error(err, kErrBadIndex, kKernelIdAttn);
 
   // ---- join the warps of the CTA ----
-  l[0] = quad_sum(l[0]);
-  l[1] = quad_sum(l[1]);
   __syncthreads();  // every ring is idle
-  float* wo = reinterpret_cast<float*>(smem) + warp * (16 * D);  // [row][channel]
-  float* wm = reinterpret_cast<float*>(smem) + kWarps * 16 * D;  // [warp][16] maxima, then sums
+  constexpr int kLd = D + 4;  // floats between rows
+  float* wo = reinterpret_cast<float*>(smem) + warp * (kRows * kLd);  // [row][channel]
+  float* wm = reinterpret_cast<float*>(smem) + kWarps * kRows * kLd;  // [warp][row] maxima, sums
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    if (t == 0) {
-      wm[warp * 16 + g + 8 * r] = m[r];
-      wm[(kWarps + warp) * 16 + g + 8 * r] = l[r];
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = 8 * nt + 2 * t + x;
+      const float sum = column_sum(l[nt][x]);
+      if (g == 0) {
+        wm[warp * kRows + row] = m[nt][x];
+        wm[(kWarps + warp) * kRows + row] = sum;
+      }
+#pragma unroll
+      for (int j = 0; j < kDTiles; ++j) {
+        wo[row * kLd + 16 * j + g] = o[nt][j][x] * v_ref;
+        wo[row * kLd + 16 * j + 8 + g] = o[nt][j][2 + x] * v_ref;
+      }
     }
-#pragma unroll
-    for (int j = 0; j < kDTiles; ++j)
-      *reinterpret_cast<float2*>(wo + (g + 8 * r) * D + 8 * j + 2 * t) =
-          make_float2(o[j][2 * r] * v_ref, o[j][2 * r + 1] * v_ref);
-  }
   __syncthreads();
   float* part = reinterpret_cast<float*>(smem + SM::part);
   float* part_ml = reinterpret_cast<float*>(smem + SM::ml);
@@ -407,15 +460,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     const int row = e / (D / 4), d = (e % (D / 4)) * 4;
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wm[w * 16 + row]);
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wm[w * kRows + row]);
     const float at = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(wm[w * 16 + row] - at);
-      sum += f * wm[(kWarps + w) * 16 + row];
-      const float4 x = *reinterpret_cast<const float4*>(all_o + (w * 16 + row) * D + d);
+      const float f = exp2f(wm[w * kRows + row] - at);
+      sum += f * wm[(kWarps + w) * kRows + row];
+      const float4 x = *reinterpret_cast<const float4*>(all_o + (w * kRows + row) * kLd + d);
       v.x += f * x.x;
       v.y += f * x.y;
       v.z += f * x.z;
@@ -462,16 +515,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   cluster.sync();  // peers keep their partials until every reader is done
 }
 
-template <int FMT, int D>
-cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream, int num_sms, unsigned* err) {
+template <int FMT, int D, int NT>
+cudaError_t launch_rows(AttnArgs a, cudaStream_t stream, int num_sms, unsigned* err) {
   using SM = AttnSmem<D>;
-  constexpr auto kern = kv8_attention_rows_kernel<FMT, D>;
+  constexpr auto kern = kv8_attention_rows_kernel<FMT, D, NT>;
+  a.row_tiles = static_cast<int>((static_cast<int64_t>(a.bt.max_new) * a.group + 8 * NT - 1) /
+                                 (8 * NT));
   static unsigned long long done = 0;  // bit d: device d
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::bytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELEASE);
   }
@@ -481,7 +538,7 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream, int num_sms, uns
   const int64_t tiles = ((static_cast<int64_t>(a.bt.max_pages) << a.c.log_page) + kTileTokens - 1) /
                         kTileTokens;
   int ks = 1;
-  while (ks < 8 && ks * 2 * kWarps <= tiles && probs * ks * 2 <= 2 * num_sms) ks *= 2;
+  while (ks < 16 && ks * 2 * kWarps <= tiles && probs * ks * 2 <= 2 * num_sms) ks *= 2;
   if (probs * ks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(probs * ks), 1, 1);
@@ -513,13 +570,21 @@ cudaError_t launch_kv8_attention(const Kv8Cache& c, const Kv8Batch& bt, const vo
   a.ldq = ldq;
   a.q_heads = q_heads;
   a.group = q_heads / c.heads;
-  a.row_tiles = static_cast<int>((static_cast<int64_t>(bt.max_new) * a.group + 15) / 16);
+  a.row_tiles = 0;
   a.scale_log2 = scale * 1.4426950408889634f;
-  if (fmt == kKvInt8)
-    return D == 64 ? launch_rows<kKvInt8, 64>(a, stream, num_sms, err)
-                   : launch_rows<kKvInt8, 128>(a, stream, num_sms, err);
-  return D == 64 ? launch_rows<kKvE4m3, 64>(a, stream, num_sms, err)
-                 : launch_rows<kKvE4m3, 128>(a, stream, num_sms, err);
+  const bool one = static_cast<int64_t>(bt.max_new) * a.group <= 8;
+  if (fmt == kKvInt8) {
+    if (D == 64)
+      return one ? launch_rows<kKvInt8, 64, 1>(a, stream, num_sms, err)
+                 : launch_rows<kKvInt8, 64, 2>(a, stream, num_sms, err);
+    return one ? launch_rows<kKvInt8, 128, 1>(a, stream, num_sms, err)
+               : launch_rows<kKvInt8, 128, 2>(a, stream, num_sms, err);
+  }
+  if (D == 64)
+    return one ? launch_rows<kKvE4m3, 64, 1>(a, stream, num_sms, err)
+               : launch_rows<kKvE4m3, 64, 2>(a, stream, num_sms, err);
+  return one ? launch_rows<kKvE4m3, 128, 1>(a, stream, num_sms, err)
+             : launch_rows<kKvE4m3, 128, 2>(a, stream, num_sms, err);
 }
 
 }  // namespace w4
