@@ -689,7 +689,7 @@ typedef struct {
  * and s0 the page's scale (0 if the page holds no earlier token of the
  * sequence):
  *   s = max(s0, up(a / qmax)), qmax 127 (int8) or 448 (e4m3), up the next
- *       value that bf16 holds;
+ *       value that bf16 holds, at least 2^-126 (0 for a = 0);
  *   new codes = round(x / s); earlier codes = round(code * s0 / s) if s > s0
  *       (ties to even; all 0 if s = 0).
  * Appending the same tokens at the same place again changes nothing.

@@ -86,9 +86,9 @@ def fp4_values(codes, scale_bytes, row, fmt):
 # ------------------------------------------------------------------- kv8 ----
 
 def round_up_bf16(t):
-    """float64 -> the next value of 8 significant bits (t >= 0, normal)."""
+    """float64 -> the next value of 8 significant bits, at least 2^-126 (0 for 0)."""
     m, e = np.frexp(t)
-    return np.ldexp(np.ceil(m * 256) / 256, e)
+    return np.where(t > 0, np.maximum(np.ldexp(np.ceil(m * 256) / 256, e), 2.0 ** -126), 0.0)
 
 
 def kv_decode(codes, fmt):

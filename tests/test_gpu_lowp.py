@@ -289,6 +289,22 @@ def test_append_bit_exact(fmt, heads, d, page, lens, news):
 
 
 @pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("exponent", [-133, -126, -112, 119])
+def test_append_extreme_magnitudes(fmt, exponent):
+    """bf16 values down to the smallest subnormals and up to the largest
+    binades, and rounding borders: integers over 127 (or 448) land on them."""
+    p = Problem(fmt, 2, 64, 32, [45], [45], q_heads=1, seed=12)
+    g = torch.Generator().manual_seed(7)
+    p.qkv = (torch.randint(-255, 256, p.qkv.shape, generator=g) * 2.0 ** exponent).to(torch.bfloat16)
+    p.ks[:], p.vs[:] = 0, 0
+    cache = p.check_append()
+    p.lens, p.news = np.array([48]), np.array([3])
+    p.starts = np.array([0, 3])
+    p.qkv = (p.qkv.double() * 1.5).to(torch.bfloat16)
+    p.check_append(cache)
+
+
+@pytest.mark.parametrize("fmt", list(KV))
 def test_append_growing_scales_and_zeros(fmt):
     """Token by token with magnitudes over 2^+-8, so that pages are rescaled
     again and again, and pages that hold only zeros."""

@@ -101,7 +101,7 @@ def test_kv8_validation(lib):
     assert append(k=None) == 1 and append(v=None) == 1
     assert append(ldk=120) == 2 and append(ldv=64) == 2
     assert append(ldk=132) == 3 and append(k=A + 8) == 3
-    assert append(rows=3000000, most=3000000) == 4      # more pages than a grid axis holds
+    assert append(rows=1 << 30, most=1 << 30, batch=1 << 10) == 4   # units of a launch
     assert attend(q=None) == 1 and attend(out=None) == 1
     assert attend(scale=float("nan")) == 1 and attend(scale=float("inf")) == 1
     assert attend(heads=3) == 2 and attend(heads=0) == 2 and attend(ldq=248) == 2

@@ -1019,8 +1019,10 @@ w4_status w4_kv8_append(const w4_kv8_cache* cache, const void* k_bf16, int64_t l
   if (st != W4_OK) return st;
   const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
   if (ldk < width || ldv < width) return W4_ERR_SHAPE;
-  // The pages that one sequence's new tokens can touch are a grid dimension.
-  if ((max_new + cache->page_size - 2) / cache->page_size + 1 > 65535) return W4_ERR_UNSUPPORTED;
+  // (page, head, side) units of the launch, counted by the most any sequence can touch.
+  const int64_t touched = (max_new + cache->page_size - 2) / cache->page_size + 1;
+  if (touched > 0x7FFFFFFF / batch || touched * batch > 0x7FFFFFFF / (2 * cache->kv_heads))
+    return W4_ERR_UNSUPPORTED;
   if (!aligned16(k_bf16) || !aligned16(v_bf16) || ldk % 8 != 0 || ldv % 8 != 0)
     return W4_ERR_ALIGNMENT;
   int sms = 0;

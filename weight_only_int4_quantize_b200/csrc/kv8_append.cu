@@ -4,20 +4,26 @@
 // magnitude of the page's new tokens and s0 the page's scale (0 where the
 // page held no earlier token of the sequence):
 //
-//   s = max(s0, up(a / qmax)),  up: the next fp32 value that bf16 holds
+//   s = max(s0, up(a / qmax)),  up: the next value that bf16 holds, at least
+//                               2^-126 (0 for a = 0)
 //   new codes      round(x / s)                (ties to even; s = 0: 0)
 //   earlier codes  round(code * s0 / s)        only where s > s0
 //
 // With s of 8 significant bits every rounding is decided exactly: a code's
-// rounding border times s has at most 16 bits, code * s0 at most 16, so a
-// product is exact in fp32 and the correctly rounded quotient lies on its
-// border only if the true one does.
+// rounding border times s has at most 16 bits (and so has code * s0), x has
+// 8, so a quotient that is not on its border is at least 2^-17 (relative) away from
+// it.  x * (1 / s), off by less than 2^-22, rounded to 20 significant bits,
+// therefore falls on the same side, and back onto the border where it is on
+// it; no division is needed.
 //
-// One CTA per (sequence, page it touches, kv head); keys and values are two
-// CTAs (blockIdx.z).  The page's new rows pass through shared memory as
-// bf16: rows are read as they lie in x, and written as they lie in the page
-// (values turned: [channel][token]).  Bound: HBM / L2 (2 bytes read and 1
-// written per element), for single tokens launch latency.
+// A warp owns 16 tokens (a granule) of one page, kv head and side; the
+// page_size / 16 warps of a page share its largest magnitude through shared
+// memory.  A lane owns D / 32 neighbouring channels of all 16 tokens: rows are
+// read coalesced, key codes leave as words of a row, and the 16 codes of a
+// channel, which lie side by side in a value row, as one 16-byte store; nothing
+// is turned in shared memory.  Bound: for prompts HBM (2 bytes read and 1
+// written per element), for single tokens the chain of dependent loads
+// (length, page id, rows and scale).
 #include "kv8.cuh"
 #include "w4_kernels.h"
 
@@ -25,18 +31,30 @@ namespace w4 {
 
 namespace {
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256;
+constexpr int kGranule = 16;
 constexpr unsigned kKernelIdAppend = 16;
 
+// v rounded to 20 significant bits.
+__device__ __forceinline__ float snap(float v) {
+  return __uint_as_float((__float_as_uint(v) + 0x8u) & 0xFFFFFFF0u);
+}
+
+// Codes of four values (in units of the scale), one per byte.
 template <int FMT>
-__device__ __forceinline__ uint32_t kv_code(float v) {
+__device__ __forceinline__ uint32_t kv_codes(float v0, float v1, float v2, float v3) {
   if constexpr (FMT == kKvInt8) {
-    const int q = __float2int_rn(v);
-    return static_cast<uint32_t>(min(127, max(-127, q))) & 0xFFu;
+    // + 1.5 * 2^23 rounds to an integer, ties to even, into the low bits.
+    // |v| <= 127 by the choice of the scale.
+    const float big = 12582912.f;
+    const uint32_t a = __byte_perm(__float_as_uint(v0 + big), __float_as_uint(v1 + big), 0x0040);
+    const uint32_t b = __byte_perm(__float_as_uint(v2 + big), __float_as_uint(v3 + big), 0x0040);
+    return __byte_perm(a, b, 0x5410);
   } else {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
-    return r & 0xFFu;
+    uint16_t a, b;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(v1), "f"(v0));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(v3), "f"(v2));
+    return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
   }
 }
 
@@ -46,108 +64,160 @@ __device__ __forceinline__ float kv_value(uint32_t code) {
     return static_cast<float>(static_cast<int8_t>(code));
   } else {
     uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code & 0xFFu)));
     return __half2float(__ushort_as_half(static_cast<uint16_t>(h & 0xFFFFu)));
   }
+}
+
+// The four codes of a word times f (= s0 / s, as s0 * (1 / s): both factors
+// are applied one after the other and only the last product is not exact).
+template <int FMT>
+__device__ __forceinline__ uint32_t rescaled(uint32_t w, float s0, float inv) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = snap(kv_value<FMT>(w >> (8 * i)) * s0 * inv);
+  return kv_codes<FMT>(v[0], v[1], v[2], v[3]);
+}
+
+// Bytes of `after` where tokens first .. first + 3 are new or rescaled
+// earlier ones, of `before` elsewhere.
+__device__ __forceinline__ uint32_t byte_mask(int first, int lo, int hi) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (first + i >= lo && first + i < hi) m |= 0xFFu << (8 * i);
+  return m;
 }
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kAppendThreads)
     kv8_append_kernel(const Kv8Cache c, const Kv8Batch bt, const __nv_bfloat16* __restrict__ k,
-                      const __nv_bfloat16* __restrict__ v, int64_t ldk, int64_t ldv,
-                      unsigned* err) {
-  // New rows [token][channel]; a row is padded by one 4-byte word so that a
-  // column walk (values) hits distinct banks.
-  extern __shared__ uint32_t tile[];
-  constexpr int kRowWords = D / 2 + 1;
+                      const __nv_bfloat16* __restrict__ v, int64_t ldk, int64_t ldv, int touched,
+                      int64_t units, unsigned* err) {
+  constexpr int CH = D / 32;  // channels of a lane
   __shared__ float red[kAppendThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int log_warps = c.log_page - 4;  // warps of a unit (page, head, side)
+  const int w = warp & ((1 << log_warps) - 1);
+  const int64_t unit = (static_cast<int64_t>(blockIdx.x) << (3 - log_warps)) + (warp >> log_warps);
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.x / c.heads, h = blockIdx.x % c.heads;
-  const bool is_v = blockIdx.z != 0;
-  const int page_size = 1 << c.log_page;
+  if (unit >= units) return;
+  const bool is_v = (unit & 1) != 0;
+  const int h = static_cast<int>((unit >> 1) % c.heads);
+  const int bj = static_cast<int>((unit >> 1) / c.heads);
+  const int b = bj / touched, jt = bj % touched;
   const Kv8Seq s = kv8_sequence(bt, b, c.log_page);
-  if (s.bad && threadIdx.x == 0 && blockIdx.y == 0) record_error(err, kErrBadIndex, kKernelIdAppend);
+  if (s.bad && lane == 0 && h == 0 && jt == 0 && !is_v && w == 0)
+    record_error(err, kErrBadIndex, kKernelIdAppend);
   const int old = s.len > s.n ? s.len - s.n : 0;
   const int skip = s.n - (s.len - old);  // new tokens in front of position 0: not held
-  const int j = (old >> c.log_page) + static_cast<int>(blockIdx.y);  // page of the sequence
+  const int j = (old >> c.log_page) + jt;  // page of the sequence
   const int64_t p0 = static_cast<int64_t>(j) << c.log_page;
-  if (s.n == 0 || p0 >= s.len) return;
+  if (s.n == 0 || p0 >= s.len) return;  // all warps of the unit
+  const int page_size = 1 << c.log_page;
   const int lo = old > p0 ? static_cast<int>(old - p0) : 0;  // new tokens [lo, hi) of the page
   const int hi = s.len - p0 < page_size ? static_cast<int>(s.len - p0) : page_size;
-  const int page = bt.table[static_cast<int64_t>(b) * bt.max_pages + j];
+  const int page = __ldg(bt.table + static_cast<int64_t>(b) * bt.max_pages + j);
   if (page < 0 || page >= c.num_pages) {
-    if (threadIdx.x == 0) record_error(err, kErrBadIndex, kKernelIdAppend);
+    if (lane == 0) record_error(err, kErrBadIndex, kKernelIdAppend);
     return;
   }
-  const int64_t row0 = static_cast<int64_t>(s.row0) + skip + (p0 + lo - old);
-  const __nv_bfloat16* x = (is_v ? v : k) + static_cast<int64_t>(h) * D;
+  const int t0 = kGranule * w;  // this warp's tokens of the page
   const int64_t ld = is_v ? ldv : ldk;
+  // Row of token t0 (only those of new tokens are read).
+  const __nv_bfloat16* x = (is_v ? v : k) + static_cast<int64_t>(h) * D + lane * CH +
+                           (static_cast<int64_t>(s.row0) + skip + (p0 + t0 - old)) * ld;
   const int64_t slot = static_cast<int64_t>(page) * c.heads + h;
-  uint8_t* out = (is_v ? c.v : c.k) + (slot << c.log_page) * D;
   float* scale = (is_v ? c.vs : c.ks) + slot;
-
-  // Rows into shared memory, and their largest magnitude.
-  const int n_new = hi - lo;
-  float amax = 0.f;
-  constexpr int kChunks = D / 8;
-  for (int e = threadIdx.x; e < n_new * kChunks; e += kAppendThreads) {
-    const int r = e / kChunks, ch = e % kChunks;
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + (row0 + r) * ld) + ch);
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      tile[r * kRowWords + 4 * ch + i] = u[i];
-      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[i] << 16)),
-                               fabsf(__uint_as_float(u[i] & 0xFFFF0000u))));
-    }
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
   const float s0 = lo > 0 ? *scale : 0.f;
-  __syncthreads();  // also: every thread has read the old scale
-#pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-  const float up = __uint_as_float(
-      (__float_as_uint(__fdiv_rn(amax, kv8_qmax(FMT))) + 0xFFFFu) & 0xFFFF0000u);
-  const float s1 = fmaxf(s0, up);
-  if (threadIdx.x == 0) *scale = s1;
 
-  const bool again = lo > 0 && s1 > s0;
-  auto element = [&](int t, int d) {  // token t of the page, channel d
-    const uint32_t u = tile[(t - lo) * kRowWords + d / 2];
-    return __uint_as_float((d & 1) ? (u & 0xFFFF0000u) : (u << 16));
-  };
-  // The page's bytes in words of four along its contiguous axis: every word
-  // that holds a new token, and those of earlier ones where the scale grew.
-  const int words = is_v ? D * page_size / 4 : hi * (D / 4);
-  const int w0 = is_v ? 0 : (again ? 0 : lo * (D / 4));
-  uint32_t* ow = reinterpret_cast<uint32_t*>(out);
-  const int log_vw = c.log_page - 2;  // words of a value row
-  for (int w = w0 + threadIdx.x; w < words; w += kAppendThreads) {
-    int t, d;
-    if (is_v) {
-      d = w >> log_vw;
-      t = (w & ((1 << log_vw) - 1)) * 4;
-      if (t >= hi || (t + 4 <= lo && !again)) continue;
-    } else {
-      t = w / (D / 4);
-      d = (w % (D / 4)) * 4;
-    }
-    const bool mixed = is_v ? t < lo || t + 4 > hi : t < lo;
-    uint32_t before = mixed ? ow[w] : 0u, after = 0u;
+  uint32_t raw[kGranule][CH / 2];
+  uint32_t big = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ti = is_v ? t + i : t, di = is_v ? d : d + i;
-      uint32_t code = (before >> (8 * i)) & 0xFFu;
-      if (ti >= lo && ti < hi)
-        code = s1 > 0.f ? kv_code<FMT>(__fdiv_rn(element(ti, di), s1)) : 0u;
-      else if (ti < lo && again)
-        code = kv_code<FMT>(__fdiv_rn(__fmul_rn(kv_value<FMT>(code), s0), s1));
-      after |= code << (8 * i);
+  for (int t = 0; t < kGranule; ++t) {
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) raw[t][i] = 0;
+    if (t0 + t >= lo && t0 + t < hi) {
+      if constexpr (CH == 4) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(x + t * ld));
+        raw[t][0] = u.x;
+        raw[t][1] = u.y;
+      } else {
+        raw[t][0] = __ldg(reinterpret_cast<const uint32_t*>(x + t * ld));
+      }
     }
-    ow[w] = after;
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) big = __vmaxu2(big, raw[t][i] & 0x7FFF7FFFu);
+  }
+  big = max(big & 0xFFFFu, big >> 16);
+  big = __reduce_max_sync(0xffffffffu, big);
+  if (log_warps > 0) {
+    if (lane == 0) red[warp] = __uint_as_float(big << 16);
+    const int id = 1 + (warp >> log_warps);
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 << log_warps) : "memory");
+    float m = 0.f;
+    for (int i = 0; i < (1 << log_warps); ++i) m = fmaxf(m, red[warp - w + i]);
+    big = __float_as_uint(m) >> 16;
+  }
+  const float amax = __uint_as_float(big << 16);
+  float up = __uint_as_float(
+      (__float_as_uint(__fdiv_rn(amax, kv8_qmax(FMT))) + 0xFFFFu) & 0xFFFF0000u);
+  if (amax > 0.f) up = fmaxf(up, __uint_as_float(0x00800000u));  // 2^-126: 1 / s is finite
+  const float s1 = fmaxf(s0, up);
+  // Every warp of the unit has read the old scale before the barrier above.
+  if (w == 0 && lane == 0) *scale = s1;
+  const float inv = s1 > 0.f ? __frcp_rn(s1) : 0.f;
+  const bool again = lo > 0 && s1 > s0;
+  const int from = again ? 0 : lo;  // bytes of tokens [from, hi) are written
+  if (t0 >= hi || t0 + kGranule <= from) return;
+
+  auto value = [&](int t, int i) {  // channel i of the lane, in units of the scale
+    const uint32_t u = raw[t][i / 2];
+    return snap(__uint_as_float((i & 1) ? (u & 0xFFFF0000u) : (u << 16)) * inv);
+  };
+  if (is_v) {
+    const bool whole = t0 >= lo && t0 + kGranule <= hi;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      uint4* dst = reinterpret_cast<uint4*>(c.v + ((slot * D + lane * CH + i) << c.log_page) + t0);
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        o[q] = kv_codes<FMT>(value(4 * q, i), value(4 * q + 1, i), value(4 * q + 2, i),
+                             value(4 * q + 3, i));
+      if (!whole) {
+        const uint4 was = *dst;
+        const uint32_t e[4] = {was.x, was.y, was.z, was.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t fresh = byte_mask(t0 + 4 * q, lo, hi);
+          const uint32_t earlier = again ? byte_mask(t0 + 4 * q, 0, lo) : 0u;
+          const uint32_t re = again ? rescaled<FMT>(e[q], s0, inv) : 0u;
+          o[q] = (o[q] & fresh) | (re & earlier) | (e[q] & ~(fresh | earlier));
+        }
+      }
+      *dst = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  } else {
+    uint8_t* row = c.k + ((slot << c.log_page) + t0) * D + lane * CH;
+#pragma unroll
+    for (int t = 0; t < kGranule; ++t) {
+      const int tok = t0 + t;
+      if (tok < from || tok >= hi) continue;
+      uint32_t code;
+      if constexpr (CH == 4) {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(row + t * D);
+        code = tok >= lo ? kv_codes<FMT>(value(t, 0), value(t, 1), value(t, 2), value(t, 3))
+                         : rescaled<FMT>(*dst, s0, inv);
+        *dst = code;
+      } else {
+        uint16_t* dst = reinterpret_cast<uint16_t*>(row + t * D);
+        code = tok >= lo ? kv_codes<FMT>(value(t, 0), value(t, 1), 0.f, 0.f)
+                         : rescaled<FMT>(*dst, s0, inv);
+        *dst = static_cast<uint16_t>(code);
+      }
+    }
   }
 }
 
@@ -156,21 +226,23 @@ cudaError_t launch_append(const Kv8Cache& c, const Kv8Batch& bt, const __nv_bflo
                           const __nv_bfloat16* v, int64_t ldk, int64_t ldv, cudaStream_t stream,
                           unsigned* err) {
   const int page = 1 << c.log_page;
-  const int touched = (bt.max_new + page - 2) / page + 1;
-  const int most = bt.max_new < page ? bt.max_new : page;
-  const size_t smem = static_cast<size_t>(most) * (D / 2 + 1) * 4;  // at most 33 KB
-  constexpr auto kern = kv8_append_kernel<FMT, D>;
+  const int touched = (bt.max_new + page - 2) / page + 1;  // pages of one sequence, at most
+  const int64_t units = static_cast<int64_t>(bt.batch) * touched * c.heads * 2;
+  const int per_cta = (kAppendThreads / 32) * kGranule / page;
+  const int64_t grid = (units + per_cta - 1) / per_cta;
+  if (grid > 0x7FFFFFFF || static_cast<int64_t>(bt.batch) * touched > 0x7FFFFFFF)
+    return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(bt.batch) * c.heads, touched, 2);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kAppendThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, c, bt, k, v, ldk, ldv, err);
+  return cudaLaunchKernelEx(&cfg, kv8_append_kernel<FMT, D>, c, bt, k, v, ldk, ldv, touched, units,
+                            err);
 }
 
 }  // namespace
