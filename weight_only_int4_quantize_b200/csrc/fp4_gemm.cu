@@ -24,6 +24,7 @@
 // Every wait is bounded; see w4_common.cuh.
 #include <cooperative_groups.h>
 #include <cudaTypedefs.h>
+#include <cstdlib>
 
 #include "fp4.cuh"
 #include "w4_kernels.h"
@@ -70,6 +71,7 @@ struct Fp4Args {
   __nv_bfloat16* y;
   int M, N, K;
   int m_tiles;
+  int tiles;  // pair kernel: all tiles
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -383,6 +385,376 @@ __global__ void __launch_bounds__(kFp4Threads)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Pair kernel (more than 256 tokens): a cluster of two CTAs computes a tile
+// of 256 output channels x NB tokens with cta_group::2 MMAs.  Each CTA holds
+// its 128 channels' codes and half of the tokens' codes, so a token tile is
+// fetched once for 256 channels.
+//
+// What bounds a large product is the traffic from L2 into shared memory: the
+// tensor pipe takes 256 channels of a 128 x 256 tile in 512 cycles, in which
+// a CTA working alone has to fetch 54 KB (nv).  Per multiply-add a pair
+// fetches 0.70 (NB = 256) or 0.59 (NB = 384) of that.  NB = 384 is two MMAs
+// of 192 columns; with the scale columns of two stages it fills TMEM (384 +
+// 2 x 64 of 512 columns).
+//
+// Persistent: one pair per two SMs walks the tiles; the loads of the next
+// tile run under the epilogue of the last (the accumulators are single).
+//
+// Loads complete on each CTA's own barriers; in the second CTA a relay thread
+// passes "stage full" on to the first, whose MMA thread issues for both.
+// MMA completion is committed to both CTAs' barriers.
+// ---------------------------------------------------------------------------
+constexpr int kPairThreads = 64 + 256;
+
+template <int FMT, int NB>
+struct PairTile {
+  static constexpr int kParts = NB > 256 ? 2 : 1;          // MMAs side by side
+  static constexpr int kPartN = NB / kParts;               // their columns
+  static constexpr int kSfTiles = NB / 128;                // scale tiles across the tokens
+  static constexpr int kWords = fp4_stage_words(FMT);
+  static constexpr uint32_t kABytes = kRows * kStageK / 2;
+  static constexpr uint32_t kPartBytes = kPartN / 2 * kStageK / 2;  // one CTA's half of a part
+  static constexpr uint32_t kBBytes = kParts * kPartBytes;
+  static constexpr uint32_t kSfaBytes = kWords * 512;
+  static constexpr uint32_t kSfbBytes = kSfTiles * kWords * 512;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+  static constexpr int kStages = static_cast<int>(222u * 1024u / kStageBytes);
+  static constexpr uint32_t kSfCols = 4 * kWords * (1 + kSfTiles);
+  static_assert(NB + 2 * kSfCols <= 512, "accumulators and two stages of scales fit TMEM");
+  static constexpr uint32_t bars = kStages * kStageBytes;
+  static constexpr uint32_t misc = bars + (3 * kStages + 3) * 8;
+  static constexpr uint32_t xrow = (misc + 16 + 15) & ~15u;  // NB token scales
+  static constexpr size_t bytes = xrow + NB * 4 + 1024;
+};
+
+__device__ __forceinline__ void pair_cp_scales(uint32_t taddr, uint32_t smem) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ void pair_umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (FMT == kFp4Mx)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on the barrier at this offset in both CTAs when the MMAs issued so
+// far have completed.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// Arrives on the barrier at this offset in CTA 0 of the pair.
+__device__ __forceinline__ void arrive_at_first(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// mbar_wait whose success also makes the peer CTA's writes visible.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort, unsigned* err) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (it == 0) t0 = globaltimer();
+    if ((it & 63u) == 63u) {
+      if (*abort) return false;
+      if (globaltimer() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        record_error(err, kErrWaitTimeout, kKernelIdFp4);
+        return false;
+      }
+    }
+  }
+}
+
+template <int FMT, int NB>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+    fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tw,
+                         const __grid_constant__ CUtensorMap tx, const Fp4Args a, int static_w,
+                         unsigned* err) {
+  using T = PairTile<FMT, NB>;
+  constexpr int S = T::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  // The dynamic shared memory starts at the same address in both CTAs, so
+  // offsets (descriptors, barriers) agree between them.
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw);
+  auto stage = [&](int s) { return base + static_cast<uint32_t>(s) * T::kStageBytes; };
+  auto full = [&](int s) { return base + T::bars + 8u * s; };
+  auto peer_full = [&](int s) { return base + T::bars + 8u * (S + s); };
+  auto empty = [&](int s) { return base + T::bars + 8u * (2 * S + s); };
+  const uint32_t acc_full = base + T::bars + 8u * (3 * S);
+  const uint32_t acc_empty = acc_full + 8u;
+  const uint32_t done_bar = acc_full + 16u;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + T::misc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + T::misc + 8);
+  float* xrow_s = reinterpret_cast<float*>(base_ptr + T::xrow);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int pairs = static_cast<int>(gridDim.x >> 1);
+  const int my_tiles = a.tiles > pair ? (a.tiles - pair + pairs - 1) / pairs : 0;
+  const int num_kb = (a.K + kStageK - 1) / kStageK;
+  const int words = a.K / (4 * fp4_block(FMT));
+  // Tile i of this pair; the token tiles of one weight tile run together.
+  auto tile_n0 = [&](int i) {
+    return ((pair + i * pairs) / a.m_tiles) * 2 * kRows + static_cast<int>(rank) * kRows;
+  };
+  auto tile_m0 = [&](int i) { return ((pair + i * pairs) % a.m_tiles) * NB; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(peer_full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 2 * 8);  // the epilogue warps of both CTAs
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tw);
+    tma_prefetch_desc(&tx);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();  // barriers of both CTAs are initialized
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA --
+    if (lane == 0) {
+      const int x_tiles = (a.M + 127) / 128;
+      const int w_tiles = (a.N + 127) / 128;
+      auto scale_bytes = [&](int kb) {  // of a row tile: fewer in a K tail
+        const int left = words - kb * T::kWords;
+        return static_cast<uint32_t>(left < T::kWords ? left : T::kWords) * 512u;
+      };
+      auto load_w = [&](int s, int n0, int kb) {
+        const uint32_t w = scale_bytes(kb);
+        mbar_arrive_expect_tx(full(s), T::kABytes + T::kBBytes + w * (1 + T::kSfTiles));
+        tma_load_2d(stage(s), &tw, kb * (kStageK / 2), n0, full(s));
+        // A row tile behind the last (N ends in the pair's first half, or a
+        // token tile ends early) gets the last one's scales: its codes are
+        // zeros and its outputs are not stored.
+        const int wt = n0 / 128 < w_tiles ? n0 / 128 : w_tiles - 1;
+        bulk_load(stage(s) + T::kABytes + T::kBBytes,
+                  a.wscales + (static_cast<int64_t>(wt) * words + kb * T::kWords) * 512, w, full(s));
+      };
+      auto load_x = [&](int s, int m0, int kb) {
+        const uint32_t w = scale_bytes(kb);
+#pragma unroll
+        for (int p = 0; p < T::kParts; ++p)
+          tma_load_2d(stage(s) + T::kABytes + p * T::kPartBytes, &tx, kb * (kStageK / 2),
+                      m0 + p * T::kPartN + static_cast<int>(rank) * (T::kPartN / 2), full(s));
+#pragma unroll
+        for (int c = 0; c < T::kSfTiles; ++c) {
+          int xt = m0 / 128 + c;
+          if (xt >= x_tiles) xt = x_tiles - 1;
+          bulk_load(stage(s) + T::kABytes + T::kBBytes + T::kSfaBytes + c * T::kWords * 512,
+                    a.xscales + (static_cast<int64_t>(xt) * words + kb * T::kWords) * 512, w,
+                    full(s));
+        }
+      };
+      // The weight's first stages may be fetched before the preceding kernel
+      // ends if the caller says that it does not write them.
+      int ahead = 0;
+      if (static_w && my_tiles > 0)
+        for (; ahead < S && ahead < num_kb; ++ahead) load_w(ahead, tile_n0(0), ahead);
+      pdl_wait();
+      int64_t issued = 0;  // stages filled (or begun) so far
+      for (int i = 0; i < my_tiles && !*abort_flag; ++i) {
+        const int n0 = tile_n0(i), m0 = tile_m0(i);
+        for (int kb = 0; kb < num_kb; ++kb, ++issued) {
+          const int s = static_cast<int>(issued % S);
+          if (issued >= S &&
+              !mbar_wait_cluster(empty(s), ((issued / S) & 1u) ^ 1u, abort_flag, err))
+            break;
+          if (issued >= ahead) load_w(s, n0, kb);
+          load_x(s, m0, kb);
+        }
+      }
+      if (*abort_flag) {
+        // Drain this CTA's own loads.  Stages whose weight part alone was
+        // begun cannot complete; they are waited for up to the limit.
+        const int64_t end = issued > ahead ? issued : ahead;
+        for (int64_t j = end - S; j < end; ++j) {
+          if (j < 0) continue;
+          volatile int dummy = 0;
+          mbar_wait(full(static_cast<int>(j % S)), (j / S) & 1u, &dummy, err, kKernelIdFp4,
+                    kWaitLimitNs / 4);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    const int64_t total = static_cast<int64_t>(my_tiles) * num_kb;
+    if (lane == 0 && rank == 1) {
+      // ---------------------------------------------------------- relay --
+      for (int64_t j = 0; j < total; ++j) {
+        const int s = static_cast<int>(j % S);
+        if (!mbar_wait(full(s), (j / S) & 1u, abort_flag, err, kKernelIdFp4)) break;
+        arrive_at_first(peer_full(s));
+      }
+    } else if (lane == 0) {
+      // ------------------------------------------------------------ MMA --
+      bool issued = false;
+      int64_t j = 0;
+      for (int i = 0; i < my_tiles && !*abort_flag; ++i) {
+        // Both CTAs have read the last tile's accumulators.
+        if (i > 0 && !mbar_wait_cluster(acc_empty, (i - 1) & 1u, abort_flag, err)) break;
+        tc_fence_after();
+        for (int kb = 0; kb < num_kb; ++kb, ++j) {
+          const int s = static_cast<int>(j % S);
+          if (!mbar_wait(full(s), (j / S) & 1u, abort_flag, err, kKernelIdFp4)) break;
+          if (!mbar_wait_cluster(peer_full(s), (j / S) & 1u, abort_flag, err)) break;
+          tc_fence_after();
+          const int left = a.K - kb * kStageK;
+          const int steps = left < kStageK ? left / 64 : kStageK / 64;
+          const int w_here = steps * T::kWords / 4;
+          const uint32_t sfa = tmem + NB + static_cast<uint32_t>(j & 1) * T::kSfCols;
+          const uint32_t sfb = sfa + 4 * T::kWords;
+          const uint32_t sf_smem = stage(s) + T::kABytes + T::kBBytes;
+#pragma unroll
+          for (int w = 0; w < T::kWords; ++w) {
+            if (w >= w_here) break;
+            pair_cp_scales(sfa + 4 * w, sf_smem + 512 * w);
+#pragma unroll
+            for (int c = 0; c < T::kSfTiles; ++c)
+              pair_cp_scales(sfb + 4 * (w * T::kSfTiles + c),
+                             sf_smem + T::kSfaBytes + 512 * (c * T::kWords + w));
+          }
+          const uint64_t da = sdesc_k_sw128(stage(s));
+          const uint64_t db = sdesc_k_sw128(stage(s) + T::kABytes);
+#pragma unroll
+          for (int kk = 0; kk < kStageK / 64; ++kk) {
+            if (kk >= steps) break;
+            const int w = FMT == kFp4Mx ? kk / 2 : kk;
+            const int id = FMT == kFp4Mx ? (kk & 1) * 2 : 0;
+            // M = 256 here: one more in the descriptor's M / 128 field.
+            const uint32_t idesc = idesc_fp4<FMT>(T::kPartN, id) + (1u << 27);
+#pragma unroll
+            for (int p = 0; p < T::kParts; ++p)
+              pair_umma<FMT>(tmem + p * T::kPartN, da + 2ull * kk,
+                             db + static_cast<uint64_t>(p * (T::kPartBytes >> 4)) + 2ull * kk,
+                             idesc, sfa + 4 * w,
+                             sfb + 4 * w * T::kSfTiles + p * (T::kPartN / 32), (kb | kk) != 0);
+          }
+          issued = true;
+          pair_commit(empty(s));
+        }
+        if (!*abort_flag) pair_commit(acc_full);
+      }
+      if (*abort_flag && issued) {
+        pair_commit(done_bar);  // in-flight MMAs end before TMEM is freed
+        volatile int dummy = 0;
+        mbar_wait(done_bar, 0, &dummy, err, kKernelIdFp4, kWaitLimitNs / 4);
+      }
+    }
+  } else {
+    // ------------------------------------------------------- epilogue --
+    const int q = warp & 3;             // TMEM lane quarter of this warp
+    const int half = (warp - 2) >> 2;   // columns [half * NB / 2, + NB / 2)
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    pdl_wait();
+    for (int i = 0; i < my_tiles; ++i) {
+      const int n = tile_n0(i) + 32 * q + lane, m0 = tile_m0(i);
+      const float wr = (a.wrow && n < a.N) ? __ldg(a.wrow + n) : 1.f;
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the last tile's scales are read
+      for (int c = threadIdx.x - 64; c < NB; c += 256)
+        xrow_s[c] = a.xrow && m0 + c < a.M ? __ldg(a.xrow + m0 + c) : 1.f;
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the eight epilogue warps
+      const bool ok = mbar_wait_cluster(acc_full, i & 1u, abort_flag, err);
+      tc_fence_after();
+      if (ok) {
+        const int c_end = half * (NB / 2) + NB / 2;
+#pragma unroll 1
+        for (int c = half * (NB / 2); c < c_end; c += 32) {
+          if (m0 + c >= a.M) break;
+          uint32_t r[2][16];
+          tmem_ld_32x32b_x16(lane_addr + c, r[0]);
+          tmem_ld_32x32b_x16(lane_addr + c + 16, r[1]);
+          tmem_ld_wait();
+          if (n < a.N) {
+            __nv_bfloat16* dst = a.y + static_cast<int64_t>(m0 + c) * a.N + n;
+            if (m0 + c + 32 <= a.M) {
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                dst[static_cast<int64_t>(x) * a.N] = __float2bfloat16_rn(
+                    __uint_as_float(r[x >> 4][x & 15]) * wr * xrow_s[c + x]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (m0 + c + x < a.M)
+                  dst[static_cast<int64_t>(x) * a.N] = __float2bfloat16_rn(
+                      __uint_as_float(r[x >> 4][x & 15]) * wr * xrow_s[c + x]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at_first(acc_empty);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster.sync();  // neither CTA's memory is in use by the other any more
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+  }
+  cluster.sync();  // both are there until both have freed their TMEM
+}
+
 CUresult encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int box_rows) {
   static PFN_cuTensorMapEncodeTiled fn = nullptr;
   if (!fn) {
@@ -455,6 +827,35 @@ cudaError_t launch(const uint8_t* xcodes, const uint8_t* wcodes, Fp4Args a, int 
   return cudaLaunchKernelEx(&cfg, kern, tw, tx, a, static_w, err);
 }
 
+template <int FMT, int NB>
+cudaError_t launch_pair(const uint8_t* xcodes, const uint8_t* wcodes, Fp4Args a, int static_w,
+                        cudaStream_t stream, int num_sms, unsigned* err) {
+  using T = PairTile<FMT, NB>;
+  constexpr auto kern = fp4_gemm_pair_kernel<FMT, NB>;
+  CUtensorMap tw, tx;
+  if (encode_codes(&tw, wcodes, a.N, a.K, kRows) != CUDA_SUCCESS ||
+      encode_codes(&tx, xcodes, a.M, a.K, T::kPartN / 2) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  cudaError_t e = opt_in_smem<kern, T::bytes>();
+  if (e != cudaSuccess) return e;
+  a.m_tiles = (a.M + NB - 1) / NB;
+  const int64_t tiles = static_cast<int64_t>((a.N + 2 * kRows - 1) / (2 * kRows)) * a.m_tiles;
+  const int64_t pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
+  if (tiles > 0x7FFFFFFF - pairs) return cudaErrorInvalidValue;
+  a.tiles = static_cast<int>(tiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), 1, 1);
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
+  cfg.dynamicSmemBytes = T::bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tw, tx, a, static_w, err);
+}
+
 template <int FMT>
 cudaError_t launch_fmt(const uint8_t* xcodes, const uint8_t* wcodes, const Fp4Args& a,
                        int static_w, cudaStream_t s, int sms, unsigned* err) {
@@ -462,7 +863,9 @@ cudaError_t launch_fmt(const uint8_t* xcodes, const uint8_t* wcodes, const Fp4Ar
   if (a.M <= 32) return launch<FMT, 32>(xcodes, wcodes, a, static_w, s, sms, err);
   if (a.M <= 64) return launch<FMT, 64>(xcodes, wcodes, a, static_w, s, sms, err);
   if (a.M <= 128) return launch<FMT, 128>(xcodes, wcodes, a, static_w, s, sms, err);
-  return launch<FMT, 256>(xcodes, wcodes, a, static_w, s, sms, err);
+  if (a.M <= 256) return launch<FMT, 256>(xcodes, wcodes, a, static_w, s, sms, err);
+  return getenv("W4_NB256") ? launch_pair<FMT, 256>(xcodes, wcodes, a, static_w, s, sms, err)
+                       : launch_pair<FMT, 384>(xcodes, wcodes, a, static_w, s, sms, err);
 }
 
 }  // namespace
@@ -481,6 +884,7 @@ cudaError_t launch_fp4_linear(const uint8_t* xcodes, const uint8_t* xscales, con
   a.N = N;
   a.K = K;
   a.m_tiles = 1;
+  a.tiles = 0;
   return fmt == kFp4Mx ? launch_fmt<kFp4Mx>(xcodes, wcodes, a, static_w, stream, num_sms, err)
                        : launch_fmt<kFp4Nv>(xcodes, wcodes, a, static_w, stream, num_sms, err);
 }
