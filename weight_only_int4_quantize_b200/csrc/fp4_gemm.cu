@@ -124,6 +124,15 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 template <int FMT, int NB>
 __global__ void __launch_bounds__(kFp4Threads)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
@@ -183,98 +192,112 @@ __global__ void __launch_bounds__(kFp4Threads)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA --
-    if (lane == 0) {
-      const int x_tiles = (a.M + 127) / 128;
-      // Scale tiles of local stage kb: fewer where the K tail ends the stage.
-      auto stage_words = [&](int kb) {
-        const int left = words - (kb_begin + kb) * T::kWords;
-        return left < T::kWords ? left : T::kWords;
-      };
-      auto load_w = [&](int kb) {
-        const int s = kb % S;
-        const uint32_t w = static_cast<uint32_t>(stage_words(kb)) * 512u;
-        mbar_arrive_expect_tx(full(s), T::kABytes + T::kBBytes + w * (1 + T::kColTiles));
-        tma_load_2d(stage(s), &tw, (kb_begin + kb) * (kStageK / 2), n0, full(s));
-        bulk_load(stage(s) + T::kABytes + T::kBBytes,
-                  a.wscales + (static_cast<int64_t>(tile_n) * words +
-                               static_cast<int64_t>(kb_begin + kb) * T::kWords) * 512,
-                  w, full(s));
-      };
-      auto load_x = [&](int kb) {
-        const int s = kb % S;
-        const uint32_t w = static_cast<uint32_t>(stage_words(kb)) * 512u;
-        tma_load_2d(stage(s) + T::kABytes, &tx, (kb_begin + kb) * (kStageK / 2), m0, full(s));
+    // The whole warp walks the stages and one elected lane issues: the
+    // operands of TMA and tcgen05 instructions stay warp-uniform.
+    const bool one = elect_one();
+    const int x_tiles = (a.M + 127) / 128;
+    auto scale_bytes = [&](int kb) {  // of a row tile: fewer in a K tail
+      const int left = words - (kb_begin + kb) * T::kWords;
+      return static_cast<uint32_t>(left < T::kWords ? left : T::kWords) * 512u;
+    };
+    auto load_w = [&](int st, int kb) {
+      const uint32_t w = scale_bytes(kb);
+      mbar_arrive_expect_tx(full(st), T::kABytes + T::kBBytes + w * (1 + T::kColTiles));
+      tma_load_2d(stage(st), &tw, (kb_begin + kb) * (kStageK / 2), n0, full(st));
+      bulk_load(stage(st) + T::kABytes + T::kBBytes,
+                a.wscales + (static_cast<int64_t>(tile_n) * words +
+                             static_cast<int64_t>(kb_begin + kb) * T::kWords) * 512,
+                w, full(st));
+    };
+    auto load_x = [&](int st, int kb) {
+      const uint32_t w = scale_bytes(kb);
+      tma_load_2d(stage(st) + T::kABytes, &tx, (kb_begin + kb) * (kStageK / 2), m0, full(st));
 #pragma unroll
-        for (int c = 0; c < T::kColTiles; ++c) {
-          // A last token tile of fewer than 129 rows has no second scale
-          // tile; the first is loaded again for columns that are not stored.
-          int xt = m0 / 128 + c;
-          if (xt >= x_tiles) xt = x_tiles - 1;
-          bulk_load(stage(s) + T::kABytes + T::kBBytes + T::kSfaBytes + c * T::kWords * 512,
-                    a.xscales + (static_cast<int64_t>(xt) * words +
-                                 static_cast<int64_t>(kb_begin + kb) * T::kWords) * 512,
-                    w, full(s));
-        }
-      };
-      const int first = num_kb < S ? num_kb : S;
-      if (!static_w) pdl_wait();
-      for (int kb = 0; kb < first; ++kb) load_w(kb);
-      if (static_w) pdl_wait();
-      for (int kb = 0; kb < first; ++kb) load_x(kb);
-      int stop = first;
-      for (int kb = first; kb < num_kb; ++kb) {
-        if (!mbar_wait(empty(kb % S), ((kb / S) & 1u) ^ 1u, abort_flag, err, kKernelIdFp4)) break;
-        load_w(kb);
-        load_x(kb);
-        stop = kb + 1;
+      for (int c = 0; c < T::kColTiles; ++c) {
+        // A last token tile of fewer than 129 rows has no second scale
+        // tile; the first is loaded again for columns that are not stored.
+        int xt = m0 / 128 + c;
+        if (xt >= x_tiles) xt = x_tiles - 1;
+        bulk_load(stage(st) + T::kABytes + T::kBBytes + T::kSfaBytes + c * T::kWords * 512,
+                  a.xscales + (static_cast<int64_t>(xt) * words +
+                               static_cast<int64_t>(kb_begin + kb) * T::kWords) * 512,
+                  w, full(st));
       }
-      if (*abort_flag) {
-        // Drain this CTA's own loads before leaving.
-        for (int kb = stop - S; kb < stop; ++kb) {
-          if (kb < 0) continue;
-          volatile int dummy = 0;
-          mbar_wait(full(kb % S), (kb / S) & 1u, &dummy, err, kKernelIdFp4, kWaitLimitNs / 4);
-        }
+    };
+    const int first = num_kb < S ? num_kb : S;
+    if (!static_w) pdl_wait();
+    for (int kb = 0; kb < first; ++kb) {
+      if (one) {
+        load_w(kb, kb);
+        if (!static_w) load_x(kb, kb);
+      }
+    }
+    if (static_w) {
+      pdl_wait();
+      for (int kb = 0; kb < first; ++kb)
+        if (one) load_x(kb, kb);
+    }
+    int st = 0;
+    uint32_t ph = 1;  // phase of stage st that is being filled
+    int kb = first;
+    for (; kb < num_kb; ++kb) {
+      if (!mbar_wait(empty(st), ph ^ 1u, abort_flag, err, kKernelIdFp4)) break;
+      if (one) {
+        load_w(st, kb);
+        load_x(st, kb);
+      }
+      if (++st == S) st = 0, ph ^= 1u;
+    }
+    if (*abort_flag && one) {
+      // Drain this CTA's own loads before leaving.
+      for (int k = kb - S; k < kb; ++k) {
+        if (k < 0) continue;
+        volatile int dummy = 0;
+        mbar_wait(full(k % S), (k / S) & 1u, &dummy, err, kKernelIdFp4, kWaitLimitNs / 4);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA --
-    if (lane == 0) {
-      bool issued = false;
-      for (int kb = 0; kb < num_kb; ++kb) {
-        const int s = kb % S;
-        if (!mbar_wait(full(s), (kb / S) & 1u, abort_flag, err, kKernelIdFp4)) break;
-        tc_fence_after();
-        const int left = a.K - (kb_begin + kb) * kStageK;
-        const int steps = left < kStageK ? left / 64 : kStageK / 64;
-        const int w_here = steps * T::kWords / 4;
-        const uint32_t sfa = tmem + NB + (kb & 1) * T::kSfCols;
-        const uint32_t sfb = sfa + 4 * T::kWords;
-        const uint32_t sf_smem = stage(s) + T::kABytes + T::kBBytes;
+    const bool one = elect_one();
+    bool issued = false;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int kb = 0; kb < num_kb; ++kb) {
+      if (!mbar_wait(full(st), ph, abort_flag, err, kKernelIdFp4)) break;
+      tc_fence_after();
+      const bool whole = a.K - (kb_begin + kb) * kStageK >= kStageK;  // else a tail of 128 channels
+      const uint32_t sfa = tmem + NB + (kb & 1) * T::kSfCols;
+      const uint32_t sfb = sfa + 4 * T::kWords;
+      const uint32_t sf_smem = stage(st) + T::kABytes + T::kBBytes;
+      const uint64_t da = sdesc_k_sw128(stage(st));
+      const uint64_t db = sdesc_k_sw128(stage(st) + T::kABytes);
+      if (one) {
 #pragma unroll
         for (int w = 0; w < T::kWords; ++w) {
-          if (w >= w_here) break;
-          tmem_cp_scales(sfa + 4 * w, sf_smem + 512 * w);
+          if (w < T::kWords / 2 || whole) {
+            tmem_cp_scales(sfa + 4 * w, sf_smem + 512 * w);
 #pragma unroll
-          for (int c = 0; c < T::kColTiles; ++c)
-            tmem_cp_scales(sfb + 4 * (w * T::kColTiles + c),
-                           sf_smem + T::kSfaBytes + 512 * (c * T::kWords + w));
+            for (int c = 0; c < T::kColTiles; ++c)
+              tmem_cp_scales(sfb + 4 * (w * T::kColTiles + c),
+                             sf_smem + T::kSfaBytes + 512 * (c * T::kWords + w));
+          }
         }
-        const uint64_t da = sdesc_k_sw128(stage(s));
-        const uint64_t db = sdesc_k_sw128(stage(s) + T::kABytes);
 #pragma unroll
         for (int kk = 0; kk < kStageK / 64; ++kk) {
-          if (kk >= steps) break;
           // 64 channels are 32 bytes (+2 in the address field); an mx scale
           // word holds two such steps, an nv word one.
           const int w = FMT == kFp4Mx ? kk / 2 : kk;
           const int id = FMT == kFp4Mx ? (kk & 1) * 2 : 0;
-          umma_fp4<FMT>(tmem, da + 2ull * kk, db + 2ull * kk, idesc_fp4<FMT>(NB, id), sfa + 4 * w,
-                        sfb + 4 * w * T::kColTiles, (kb | kk) != 0);
+          if (kk < kStageK / 128 || whole)
+            umma_fp4<FMT>(tmem, da + 2ull * kk, db + 2ull * kk, idesc_fp4<FMT>(NB, id), sfa + 4 * w,
+                          sfb + 4 * w * T::kColTiles, (kb | kk) != 0);
         }
-        issued = true;
-        umma_commit(empty(s));
+        umma_commit(empty(st));
       }
+      issued = true;
+      if (++st == S) st = 0, ph ^= 1u;
+    }
+    if (one) {
       if (!*abort_flag) {
         umma_commit(acc_full);
       } else if (issued) {
@@ -401,9 +424,16 @@ __global__ void __launch_bounds__(kFp4Threads)
 // Persistent: one pair per two SMs walks the tiles; the loads of the next
 // tile run under the epilogue of the last (the accumulators are single).
 //
-// Loads complete on each CTA's own barriers; in the second CTA a relay thread
-// passes "stage full" on to the first, whose MMA thread issues for both.
-// MMA completion is committed to both CTAs' barriers.
+// Both CTAs' loads complete on the first CTA's barrier of the stage, whose
+// MMA warp issues for both (all loads are tensor-map loads, which may signal
+// the peer's barrier; scale tiles are rows of 256 words).  MMA completion is
+// committed to both CTAs' barriers.
+//
+// Issue order and uniformity matter as much as bandwidth: with the MMA loop
+// under `lane == 0` every tcgen05 operand went through a vector register and
+// one pair alone took 1.16 us per stage (NB = 384, nv); with the warp walking
+// the loop and an elected lane issuing, 0.62 us; with a relay thread passing
+// "stage full" to the first CTA replaced by direct signals, see below.
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 64 + 256;
 
@@ -423,7 +453,7 @@ struct PairTile {
   static constexpr uint32_t kSfCols = 4 * kWords * (1 + kSfTiles);
   static_assert(NB + 2 * kSfCols <= 512, "accumulators and two stages of scales fit TMEM");
   static constexpr uint32_t bars = kStages * kStageBytes;
-  static constexpr uint32_t misc = bars + (3 * kStages + 3) * 8;
+  static constexpr uint32_t misc = bars + (2 * kStages + 3) * 8;
   static constexpr uint32_t xrow = (misc + 16 + 15) & ~15u;  // NB token scales
   static constexpr size_t bytes = xrow + NB * 4 + 1024;
 };
@@ -473,6 +503,22 @@ __device__ __forceinline__ void arrive_at_first(uint32_t bar) {
       : "memory");
 }
 
+// 2-D tiled load into this CTA's shared memory, completion counted on the
+// barrier at this offset in CTA 0 of the pair (`bar`: its cluster address).
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+
 // mbar_wait whose success also makes the peer CTA's writes visible.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
                                                   volatile int* abort, unsigned* err) {
@@ -502,7 +548,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 template <int FMT, int NB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tw,
-                         const __grid_constant__ CUtensorMap tx, const Fp4Args a, int static_w,
+                         const __grid_constant__ CUtensorMap tx,
+                         const __grid_constant__ CUtensorMap tws,
+                         const __grid_constant__ CUtensorMap txs, const Fp4Args a, int static_w,
                          unsigned* err) {
   using T = PairTile<FMT, NB>;
   constexpr int S = T::kStages;
@@ -514,9 +562,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   uint8_t* base_ptr = smem_raw + (base - raw);
   auto stage = [&](int s) { return base + static_cast<uint32_t>(s) * T::kStageBytes; };
   auto full = [&](int s) { return base + T::bars + 8u * s; };
-  auto peer_full = [&](int s) { return base + T::bars + 8u * (S + s); };
-  auto empty = [&](int s) { return base + T::bars + 8u * (2 * S + s); };
-  const uint32_t acc_full = base + T::bars + 8u * (3 * S);
+  auto empty = [&](int s) { return base + T::bars + 8u * (S + s); };
+  const uint32_t acc_full = base + T::bars + 8u * (2 * S);
   const uint32_t acc_empty = acc_full + 8u;
   const uint32_t done_bar = acc_full + 16u;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + T::misc);
@@ -531,7 +578,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   const int pairs = static_cast<int>(gridDim.x >> 1);
   const int my_tiles = a.tiles > pair ? (a.tiles - pair + pairs - 1) / pairs : 0;
   const int num_kb = (a.K + kStageK - 1) / kStageK;
-  const int words = a.K / (4 * fp4_block(FMT));
   // Tile i of this pair; the token tiles of one weight tile run together.
   auto tile_n0 = [&](int i) {
     return ((pair + i * pairs) / a.m_tiles) * 2 * kRows + static_cast<int>(rank) * kRows;
@@ -541,7 +587,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(peer_full(s), 1);
       mbar_init(empty(s), 1);
     }
     mbar_init(acc_full, 1);
@@ -553,6 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tw);
     tma_prefetch_desc(&tx);
+    tma_prefetch_desc(&tws);
+    tma_prefetch_desc(&txs);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -569,128 +616,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA --
-    if (lane == 0) {
-      const int x_tiles = (a.M + 127) / 128;
-      const int w_tiles = (a.N + 127) / 128;
-      auto scale_bytes = [&](int kb) {  // of a row tile: fewer in a K tail
-        const int left = words - kb * T::kWords;
-        return static_cast<uint32_t>(left < T::kWords ? left : T::kWords) * 512u;
-      };
-      auto load_w = [&](int s, int n0, int kb) {
-        const uint32_t w = scale_bytes(kb);
-        mbar_arrive_expect_tx(full(s), T::kABytes + T::kBBytes + w * (1 + T::kSfTiles));
-        tma_load_2d(stage(s), &tw, kb * (kStageK / 2), n0, full(s));
-        // A row tile behind the last (N ends in the pair's first half, or a
-        // token tile ends early) gets the last one's scales: its codes are
-        // zeros and its outputs are not stored.
-        const int wt = n0 / 128 < w_tiles ? n0 / 128 : w_tiles - 1;
-        bulk_load(stage(s) + T::kABytes + T::kBBytes,
-                  a.wscales + (static_cast<int64_t>(wt) * words + kb * T::kWords) * 512, w, full(s));
-      };
-      auto load_x = [&](int s, int m0, int kb) {
-        const uint32_t w = scale_bytes(kb);
+    const bool one = elect_one();
+    const uint32_t full0 = in_first(full(0));
+    // Boxes that reach over the end of a tensor (K tail, last row tiles) are
+    // filled with zeros and count in full.
+    auto load_w = [&](int st, int n0, int kb) {
+      if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * T::kStageBytes);
+      pair_load_2d(stage(st), &tw, kb * (kStageK / 2), n0, full0 + 8u * st);
+      pair_load_2d(stage(st) + T::kABytes + T::kBBytes, &tws, kb * 256, n0 / 128, full0 + 8u * st);
+    };
+    auto load_x = [&](int st, int m0, int kb) {
 #pragma unroll
-        for (int p = 0; p < T::kParts; ++p)
-          tma_load_2d(stage(s) + T::kABytes + p * T::kPartBytes, &tx, kb * (kStageK / 2),
-                      m0 + p * T::kPartN + static_cast<int>(rank) * (T::kPartN / 2), full(s));
-#pragma unroll
-        for (int c = 0; c < T::kSfTiles; ++c) {
-          int xt = m0 / 128 + c;
-          if (xt >= x_tiles) xt = x_tiles - 1;
-          bulk_load(stage(s) + T::kABytes + T::kBBytes + T::kSfaBytes + c * T::kWords * 512,
-                    a.xscales + (static_cast<int64_t>(xt) * words + kb * T::kWords) * 512, w,
-                    full(s));
+      for (int p = 0; p < T::kParts; ++p)
+        pair_load_2d(stage(st) + T::kABytes + p * T::kPartBytes, &tx, kb * (kStageK / 2),
+                     m0 + p * T::kPartN + static_cast<int>(rank) * (T::kPartN / 2),
+                     full0 + 8u * st);
+      pair_load_2d(stage(st) + T::kABytes + T::kBBytes + T::kSfaBytes, &txs, kb * 256, m0 / 128,
+                   full0 + 8u * st);
+    };
+    // The weight's first stages may be fetched before the preceding kernel
+    // ends if the caller says that it does not write them.
+    int ahead = 0;
+    if (static_w && my_tiles > 0)
+      for (; ahead < S && ahead < num_kb; ++ahead)
+        if (one) load_w(ahead, tile_n0(0), ahead);
+    pdl_wait();
+    int st = 0, filled = 0;  // next stage; stages begun, counted up to S
+    uint32_t ph = 0;         // phase of stage st that is being filled
+    for (int i = 0; i < my_tiles && !*abort_flag; ++i) {
+      const int n0 = tile_n0(i), m0 = tile_m0(i);
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (filled == S) {
+          if (!mbar_wait_cluster(empty(st), ph ^ 1u, abort_flag, err)) break;
+        } else {
+          ++filled;
         }
-      };
-      // The weight's first stages may be fetched before the preceding kernel
-      // ends if the caller says that it does not write them.
-      int ahead = 0;
-      if (static_w && my_tiles > 0)
-        for (; ahead < S && ahead < num_kb; ++ahead) load_w(ahead, tile_n0(0), ahead);
-      pdl_wait();
-      int64_t issued = 0;  // stages filled (or begun) so far
-      for (int i = 0; i < my_tiles && !*abort_flag; ++i) {
-        const int n0 = tile_n0(i), m0 = tile_m0(i);
-        for (int kb = 0; kb < num_kb; ++kb, ++issued) {
-          const int s = static_cast<int>(issued % S);
-          if (issued >= S &&
-              !mbar_wait_cluster(empty(s), ((issued / S) & 1u) ^ 1u, abort_flag, err))
-            break;
-          if (issued >= ahead) load_w(s, n0, kb);
-          load_x(s, m0, kb);
+        if (one) {
+          if (i > 0 || kb >= ahead) load_w(st, n0, kb);
+          load_x(st, m0, kb);
         }
+        if (++st == S) st = 0, ph ^= 1u;
       }
-      if (*abort_flag) {
-        // Drain this CTA's own loads.  Stages whose weight part alone was
-        // begun cannot complete; they are waited for up to the limit.
-        const int64_t end = issued > ahead ? issued : ahead;
-        for (int64_t j = end - S; j < end; ++j) {
-          if (j < 0) continue;
-          volatile int dummy = 0;
-          mbar_wait(full(static_cast<int>(j % S)), (j / S) & 1u, &dummy, err, kKernelIdFp4,
-                    kWaitLimitNs / 4);
-        }
+    }
+    if (*abort_flag && one && rank == 0) {
+      // Drain both CTAs' loads: of each stage, the fill begun last.  A fill
+      // that the peer did not begin cannot complete; it is waited for up to
+      // the limit.
+      for (int k = 0; k < (ahead > filled ? ahead : filled); ++k) {
+        volatile int dummy = 0;
+        mbar_wait(full(k), k < st ? ph : ph ^ (filled == S ? 1u : 0u), &dummy, err, kKernelIdFp4,
+                  kWaitLimitNs / 4);
       }
     }
   } else if (warp == 1) {
-    const int64_t total = static_cast<int64_t>(my_tiles) * num_kb;
-    if (lane == 0 && rank == 1) {
-      // ---------------------------------------------------------- relay --
-      for (int64_t j = 0; j < total; ++j) {
-        const int s = static_cast<int>(j % S);
-        if (!mbar_wait(full(s), (j / S) & 1u, abort_flag, err, kKernelIdFp4)) break;
-        arrive_at_first(peer_full(s));
-      }
-    } else if (lane == 0) {
+    // The whole warp walks the stages and one elected lane issues: the
+    // operands of the tcgen05 instructions stay warp-uniform.
+    const bool one = elect_one();
+    if (rank == 0) {
       // ------------------------------------------------------------ MMA --
       bool issued = false;
-      int64_t j = 0;
+      int st = 0;
+      uint32_t ph = 0, buf = 0;
       for (int i = 0; i < my_tiles && !*abort_flag; ++i) {
         // Both CTAs have read the last tile's accumulators.
         if (i > 0 && !mbar_wait_cluster(acc_empty, (i - 1) & 1u, abort_flag, err)) break;
         tc_fence_after();
-        for (int kb = 0; kb < num_kb; ++kb, ++j) {
-          const int s = static_cast<int>(j % S);
-          if (!mbar_wait(full(s), (j / S) & 1u, abort_flag, err, kKernelIdFp4)) break;
-          if (!mbar_wait_cluster(peer_full(s), (j / S) & 1u, abort_flag, err)) break;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait_cluster(full(st), ph, abort_flag, err)) break;
           tc_fence_after();
-          const int left = a.K - kb * kStageK;
-          const int steps = left < kStageK ? left / 64 : kStageK / 64;
-          const int w_here = steps * T::kWords / 4;
-          const uint32_t sfa = tmem + NB + static_cast<uint32_t>(j & 1) * T::kSfCols;
+          const uint32_t sfa = tmem + NB + buf * T::kSfCols;
           const uint32_t sfb = sfa + 4 * T::kWords;
-          const uint32_t sf_smem = stage(s) + T::kABytes + T::kBBytes;
+          const uint32_t sf_smem = stage(st) + T::kABytes + T::kBBytes;
+          const uint64_t da = sdesc_k_sw128(stage(st));
+          const uint64_t db = sdesc_k_sw128(stage(st) + T::kABytes);
+          const bool whole = a.K - kb * kStageK >= kStageK;  // else a tail of 128 channels
+          if (one) {
 #pragma unroll
-          for (int w = 0; w < T::kWords; ++w) {
-            if (w >= w_here) break;
-            pair_cp_scales(sfa + 4 * w, sf_smem + 512 * w);
+            for (int w = 0; w < T::kWords; ++w) {
+              if (w < T::kWords / 2 || whole) {
+                pair_cp_scales(sfa + 4 * w, sf_smem + 512 * w);
 #pragma unroll
-            for (int c = 0; c < T::kSfTiles; ++c)
-              pair_cp_scales(sfb + 4 * (w * T::kSfTiles + c),
-                             sf_smem + T::kSfaBytes + 512 * (c * T::kWords + w));
-          }
-          const uint64_t da = sdesc_k_sw128(stage(s));
-          const uint64_t db = sdesc_k_sw128(stage(s) + T::kABytes);
+                for (int c = 0; c < T::kSfTiles; ++c)
+                  pair_cp_scales(sfb + 4 * (w * T::kSfTiles + c),
+                                 sf_smem + T::kSfaBytes + 512 * (c * T::kWords + w));
+              }
+            }
 #pragma unroll
-          for (int kk = 0; kk < kStageK / 64; ++kk) {
-            if (kk >= steps) break;
-            const int w = FMT == kFp4Mx ? kk / 2 : kk;
-            const int id = FMT == kFp4Mx ? (kk & 1) * 2 : 0;
-            // M = 256 here: one more in the descriptor's M / 128 field.
-            const uint32_t idesc = idesc_fp4<FMT>(T::kPartN, id) + (1u << 27);
+            for (int kk = 0; kk < kStageK / 64; ++kk) {
+              const int w = FMT == kFp4Mx ? kk / 2 : kk;
+              const int id = FMT == kFp4Mx ? (kk & 1) * 2 : 0;
+              // M = 256 here: one more in the descriptor's M / 128 field.
+              const uint32_t idesc = idesc_fp4<FMT>(T::kPartN, id) + (1u << 27);
+              if (kk < kStageK / 128 || whole) {
 #pragma unroll
-            for (int p = 0; p < T::kParts; ++p)
-              pair_umma<FMT>(tmem + p * T::kPartN, da + 2ull * kk,
-                             db + static_cast<uint64_t>(p * (T::kPartBytes >> 4)) + 2ull * kk,
-                             idesc, sfa + 4 * w,
-                             sfb + 4 * w * T::kSfTiles + p * (T::kPartN / 32), (kb | kk) != 0);
+                for (int p = 0; p < T::kParts; ++p)
+                  pair_umma<FMT>(tmem + p * T::kPartN, da + 2ull * kk,
+                                 db + static_cast<uint64_t>(p * (T::kPartBytes >> 4)) + 2ull * kk,
+                                 idesc, sfa + 4 * w,
+                                 sfb + 4 * w * T::kSfTiles + p * (T::kPartN / 32), (kb | kk) != 0);
+              }
+            }
+            pair_commit(empty(st));
           }
           issued = true;
-          pair_commit(empty(s));
+          buf ^= 1u;
+          if (++st == S) st = 0, ph ^= 1u;
         }
-        if (!*abort_flag) pair_commit(acc_full);
+        if (one && !*abort_flag) pair_commit(acc_full);
       }
-      if (*abort_flag && issued) {
+      if (*abort_flag && issued && one) {
         pair_commit(done_bar);  // in-flight MMAs end before TMEM is freed
         volatile int dummy = 0;
         mbar_wait(done_bar, 0, &dummy, err, kKernelIdFp4, kWaitLimitNs / 4);
@@ -755,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   cluster.sync();  // both are there until both have freed their TMEM
 }
 
-CUresult encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int box_rows) {
+PFN_cuTensorMapEncodeTiled encode_fn() {
   static PFN_cuTensorMapEncodeTiled fn = nullptr;
   if (!fn) {
     cudaDriverEntryPointQueryResult q;
@@ -763,9 +797,16 @@ CUresult encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t 
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
             cudaSuccess ||
         q != cudaDriverEntryPointSuccess || !p)
-      return CUDA_ERROR_NOT_FOUND;
+      return nullptr;
     fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled>(p);
   }
+  return fn;
+}
+
+// Codes [rows, K / 2]: boxes of one stage's 128 bytes by box_rows.
+CUresult encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
   const cuuint32_t box[2] = {kStageK / 2, static_cast<cuuint32_t>(box_rows)};
@@ -773,6 +814,24 @@ CUresult encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t 
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// Scale tiles [row tiles, K words of 512 bytes]: boxes of one stage's tiles
+// (1024 or 2048 bytes, as 256 elements of 4 or 8) by box_tiles row tiles.
+CUresult encode_scales(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int fmt,
+                       int box_tiles) {
+  const PFN_cuTensorMapEncodeTiled fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  const cuuint64_t elem = fmt == kFp4Mx ? 4 : 8;
+  const cuuint64_t bytes = static_cast<cuuint64_t>(K / (4 * fp4_block(fmt))) * 512;
+  const cuuint64_t dims[2] = {bytes / elem, static_cast<cuuint64_t>((rows + 127) / 128)};
+  const cuuint64_t strides[1] = {bytes};
+  const cuuint32_t box[2] = {256, static_cast<cuuint32_t>(box_tiles)};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(map, fmt == kFp4Mx ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT64, 2,
+            const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <auto kern, size_t kBytes>
@@ -832,9 +891,11 @@ cudaError_t launch_pair(const uint8_t* xcodes, const uint8_t* wcodes, Fp4Args a,
                         cudaStream_t stream, int num_sms, unsigned* err) {
   using T = PairTile<FMT, NB>;
   constexpr auto kern = fp4_gemm_pair_kernel<FMT, NB>;
-  CUtensorMap tw, tx;
+  CUtensorMap tw, tx, tws, txs;
   if (encode_codes(&tw, wcodes, a.N, a.K, kRows) != CUDA_SUCCESS ||
-      encode_codes(&tx, xcodes, a.M, a.K, T::kPartN / 2) != CUDA_SUCCESS)
+      encode_codes(&tx, xcodes, a.M, a.K, T::kPartN / 2) != CUDA_SUCCESS ||
+      encode_scales(&tws, a.wscales, a.N, a.K, FMT, 1) != CUDA_SUCCESS ||
+      encode_scales(&txs, a.xscales, a.M, a.K, FMT, T::kSfTiles) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   cudaError_t e = opt_in_smem<kern, T::bytes>();
   if (e != cudaSuccess) return e;
@@ -853,7 +914,7 @@ cudaError_t launch_pair(const uint8_t* xcodes, const uint8_t* wcodes, Fp4Args a,
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tw, tx, a, static_w, err);
+  return cudaLaunchKernelEx(&cfg, kern, tw, tx, tws, txs, a, static_w, err);
 }
 
 template <int FMT>
