@@ -8,10 +8,10 @@
 // (the row scales only for nv; applied to the fp32 sum, then one rounding to
 // bf16).
 //
-// The weight is always the A operand (128 output channels per tile) and the
-// tokens the B operand (NB = 16 ... 256 columns), so one kernel serves a
-// single token and a prefill: a decode step streams the weight once through
-// tiles of 16 token columns.  A stage is 256 channels: 128-byte rows of
+// The weight is always the A operand and the tokens the B operand: up to 128
+// tokens a CTA takes 128 output channels x NB = 16 ... 128 token columns, so
+// a decode step streams the weight once through tiles of 16 columns; above,
+// two CTAs work on 256 channels x 256 or 384 tokens (pair kernel, below).  A stage is 256 channels: 128-byte rows of
 // codes (TMA, 128-byte swizzle) and 2 (mx) or 4 (nv) scale tiles of 512
 // bytes per 128 rows, copied to shared memory in one piece and to TMEM by
 // tcgen05.cp, which the tensor pipe runs in order with the MMAs.  A K tail
@@ -24,7 +24,6 @@
 // Every wait is bounded; see w4_common.cuh.
 #include <cooperative_groups.h>
 #include <cudaTypedefs.h>
-#include <cstdlib>
 
 #include "fp4.cuh"
 #include "w4_kernels.h"
@@ -43,21 +42,20 @@ constexpr unsigned kKernelIdFp4 = 8;
 
 template <int FMT, int NB>
 struct Fp4Tile {
-  static constexpr int kColTiles = NB > 128 ? NB / 128 : 1;  // scale tiles across the tokens
+  static_assert(NB <= 128, "one scale tile across the tokens");
   static constexpr int kWords = fp4_stage_words(FMT);
   static constexpr uint32_t kABytes = kRows * kStageK / 2;
   static constexpr uint32_t kBBytes = NB * kStageK / 2;
   static constexpr uint32_t kSfaBytes = kWords * 512;
-  static constexpr uint32_t kSfbBytes = kColTiles * kWords * 512;
+  static constexpr uint32_t kSfbBytes = kWords * 512;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-  // Two CTAs share an SM unless the token tile is 256 wide.
-  static constexpr int kCtasPerSm = NB > 128 ? 1 : 2;
-  static constexpr int kStages =
-      static_cast<int>((kCtasPerSm == 1 ? 222u * 1024u : 109u * 1024u) / kStageBytes);
+  static constexpr int kMinSplitKb = NB <= 32 ? 6 : NB == 64 ? 4 : 2;
+  static constexpr int kStages = static_cast<int>(109u * 1024u / kStageBytes);  // two CTAs per SM
   // TMEM: NB accumulator columns, then the scale columns of two stages.
-  static constexpr uint32_t kSfCols = 4 * kWords * (1 + kColTiles);
+  static constexpr uint32_t kSfCols = 4 * kWords * 2;
   static constexpr uint32_t kUsed = NB + 2 * kSfCols;
-  static constexpr uint32_t kTmemCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static constexpr uint32_t kTmemCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
+  static_assert(kUsed <= 256, "two CTAs' TMEM fits an SM");
   static constexpr uint32_t bars = kStages * kStageBytes;
   static constexpr uint32_t misc = bars + (2 * kStages + 2) * 8;
   static constexpr size_t bytes = misc + 16 + 1024;  // + alignment
@@ -189,20 +187,23 @@ __global__ void __launch_bounds__(kFp4Threads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // The next kernel may be scheduled from here on: not before this CTA holds
+  // its TMEM, or a dependent that allocated first would wait for this kernel
+  // while this CTA waits for its TMEM.
+  if (threadIdx.x == 0) pdl_launch_dependents();
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA --
     // The whole warp walks the stages and one elected lane issues: the
     // operands of TMA and tcgen05 instructions stay warp-uniform.
     const bool one = elect_one();
-    const int x_tiles = (a.M + 127) / 128;
     auto scale_bytes = [&](int kb) {  // of a row tile: fewer in a K tail
       const int left = words - (kb_begin + kb) * T::kWords;
       return static_cast<uint32_t>(left < T::kWords ? left : T::kWords) * 512u;
     };
     auto load_w = [&](int st, int kb) {
       const uint32_t w = scale_bytes(kb);
-      mbar_arrive_expect_tx(full(st), T::kABytes + T::kBBytes + w * (1 + T::kColTiles));
+      mbar_arrive_expect_tx(full(st), T::kABytes + T::kBBytes + 2 * w);
       tma_load_2d(stage(st), &tw, (kb_begin + kb) * (kStageK / 2), n0, full(st));
       bulk_load(stage(st) + T::kABytes + T::kBBytes,
                 a.wscales + (static_cast<int64_t>(tile_n) * words +
@@ -212,17 +213,10 @@ __global__ void __launch_bounds__(kFp4Threads)
     auto load_x = [&](int st, int kb) {
       const uint32_t w = scale_bytes(kb);
       tma_load_2d(stage(st) + T::kABytes, &tx, (kb_begin + kb) * (kStageK / 2), m0, full(st));
-#pragma unroll
-      for (int c = 0; c < T::kColTiles; ++c) {
-        // A last token tile of fewer than 129 rows has no second scale
-        // tile; the first is loaded again for columns that are not stored.
-        int xt = m0 / 128 + c;
-        if (xt >= x_tiles) xt = x_tiles - 1;
-        bulk_load(stage(st) + T::kABytes + T::kBBytes + T::kSfaBytes + c * T::kWords * 512,
-                  a.xscales + (static_cast<int64_t>(xt) * words +
-                               static_cast<int64_t>(kb_begin + kb) * T::kWords) * 512,
-                  w, full(st));
-      }
+      bulk_load(stage(st) + T::kABytes + T::kBBytes + T::kSfaBytes,
+                a.xscales + (static_cast<int64_t>(m0 / 128) * words +
+                             static_cast<int64_t>(kb_begin + kb) * T::kWords) * 512,
+                w, full(st));
     };
     const int first = num_kb < S ? num_kb : S;
     if (!static_w) pdl_wait();
@@ -276,10 +270,7 @@ __global__ void __launch_bounds__(kFp4Threads)
         for (int w = 0; w < T::kWords; ++w) {
           if (w < T::kWords / 2 || whole) {
             tmem_cp_scales(sfa + 4 * w, sf_smem + 512 * w);
-#pragma unroll
-            for (int c = 0; c < T::kColTiles; ++c)
-              tmem_cp_scales(sfb + 4 * (w * T::kColTiles + c),
-                             sf_smem + T::kSfaBytes + 512 * (c * T::kWords + w));
+            tmem_cp_scales(sfb + 4 * w, sf_smem + T::kSfaBytes + 512 * w);
           }
         }
 #pragma unroll
@@ -290,7 +281,7 @@ __global__ void __launch_bounds__(kFp4Threads)
           const int id = FMT == kFp4Mx ? (kk & 1) * 2 : 0;
           if (kk < kStageK / 128 || whole)
             umma_fp4<FMT>(tmem, da + 2ull * kk, db + 2ull * kk, idesc_fp4<FMT>(NB, id), sfa + 4 * w,
-                          sfb + 4 * w * T::kColTiles, (kb | kk) != 0);
+                          sfb + 4 * w, (kb | kk) != 0);
         }
         umma_commit(empty(st));
       }
@@ -400,7 +391,6 @@ __global__ void __launch_bounds__(kFp4Threads)
   }
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) pdl_launch_dependents();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -613,6 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   cluster.sync();  // barriers of both CTAs are initialized
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0) pdl_launch_dependents();  // holds its TMEM, as above
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA --
@@ -779,7 +770,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   __syncwarp();
   tc_fence_before();
   cluster.sync();  // neither CTA's memory is in use by the other any more
-  if (threadIdx.x == 0) pdl_launch_dependents();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -849,6 +839,20 @@ cudaError_t opt_in_smem() {
   return cudaSuccess;
 }
 
+// CTAs that split K: enough to fill the GPU (clusters of odd sizes do not pack
+// to the last slot, so 264 of 296 at two per SM), each keeping at least
+// `min_kb` stages, under which the ring is latency-bound anyway and the join
+// of the partial tiles (0.5 us for 16 tokens, several for 128) is lost time.
+// Measured at one token: 5120 x 17408 19.5 us unsplit, 13.9 / 12.4 / 12.0 by
+// 2 / 4 / 6; 6144 x 2048 5.4 unsplit, 6.0 / 6.3 by 2 / 4; 17408 x 5120 11.8
+// unsplit, 12.4 by 2.  At 128 tokens 2048 x 2048: 12.5 unsplit, 8.4 by 4.
+int k_split(int64_t tiles, int num_kb, int min_kb, int num_sms) {
+  const int64_t fit = static_cast<int64_t>(num_sms) * 264 / 148 / tiles;
+  int ks = num_kb / min_kb;
+  if (ks > fit) ks = static_cast<int>(fit);
+  return ks < 1 ? 1 : ks > kMaxSplit ? kMaxSplit : ks;
+}
+
 template <int FMT, int NB>
 cudaError_t launch(const uint8_t* xcodes, const uint8_t* wcodes, Fp4Args a, int static_w,
                    cudaStream_t stream, int num_sms, unsigned* err) {
@@ -863,10 +867,7 @@ cudaError_t launch(const uint8_t* xcodes, const uint8_t* wcodes, Fp4Args a, int 
   a.m_tiles = (a.M + NB - 1) / NB;
   const int64_t tiles = static_cast<int64_t>((a.N + kRows - 1) / kRows) * a.m_tiles;
   const int num_kb = (a.K + kStageK - 1) / kStageK;
-  // K is split while the CTAs still fit the GPU at once.
-  int ks = 1;
-  const int64_t slots = static_cast<int64_t>(num_sms) * T::kCtasPerSm;
-  while (ks < kMaxSplit && ks < num_kb && tiles * (ks + 1) <= slots) ++ks;
+  const int ks = k_split(tiles, num_kb, T::kMinSplitKb, num_sms);
   static_assert(NB * kRows * 4 <= T::kStages * T::kStageBytes, "a partial tile fits the stages");
   if (tiles * ks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -917,16 +918,42 @@ cudaError_t launch_pair(const uint8_t* xcodes, const uint8_t* wcodes, Fp4Args a,
   return cudaLaunchKernelEx(&cfg, kern, tw, tx, tws, txs, a, static_w, err);
 }
 
+// Above 128 tokens: the pair kernel with 256 or 384 token columns, or, where
+// that leaves most SMs idle over a long K, the single-CTA kernel with 128
+// columns and K split over a cluster.  Time model in microseconds, fitted to
+// launches of 200 ... 8192 tokens on 148 SMs (within 12 %): waves x (stages x
+// per-stage cost + epilogue), plus the join of a split's partial tiles.
+// 5120 x 17408 at 200 tokens: pair 25.0, split 19.9; 11008 x 4096 at 200:
+// 10.7, 19.3; 8192 tokens x 5120 x 17408: 256 columns 263, 384 columns 249;
+// 1999 x 11008 x 4096: 43, 47.
+int large_shape(int M, int N, int num_kb, int num_sms) {
+  auto waves = [](int64_t tiles, int64_t slots) {
+    return static_cast<double>((tiles + slots - 1) / slots);
+  };
+  const int64_t pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
+  const int64_t wide = (N + 255) / 256;
+  const double p256 = waves(wide * ((M + 255) / 256), pairs) * (0.39 * num_kb + 2.0);
+  const double p384 = waves(wide * ((M + 383) / 384), pairs) * (0.57 * num_kb + 3.0);
+  const int64_t tiles = static_cast<int64_t>((N + 127) / 128) * ((M + 127) / 128);
+  const int64_t slots = 2 * static_cast<int64_t>(num_sms);
+  const int ks = k_split(tiles, num_kb, 2, num_sms);
+  const double split =
+      waves(tiles * ks, slots) * (0.4 * ((num_kb + ks - 1) / ks) + 2.0) + (ks > 1 ? 5.0 : 0.0);
+  if (split < p256 && split < p384) return 128;
+  return p384 < p256 ? 384 : 256;
+}
+
 template <int FMT>
 cudaError_t launch_fmt(const uint8_t* xcodes, const uint8_t* wcodes, const Fp4Args& a,
                        int static_w, cudaStream_t s, int sms, unsigned* err) {
   if (a.M <= 16) return launch<FMT, 16>(xcodes, wcodes, a, static_w, s, sms, err);
   if (a.M <= 32) return launch<FMT, 32>(xcodes, wcodes, a, static_w, s, sms, err);
   if (a.M <= 64) return launch<FMT, 64>(xcodes, wcodes, a, static_w, s, sms, err);
-  if (a.M <= 128) return launch<FMT, 128>(xcodes, wcodes, a, static_w, s, sms, err);
-  if (a.M <= 256) return launch<FMT, 256>(xcodes, wcodes, a, static_w, s, sms, err);
-  return getenv("W4_NB256") ? launch_pair<FMT, 256>(xcodes, wcodes, a, static_w, s, sms, err)
-                       : launch_pair<FMT, 384>(xcodes, wcodes, a, static_w, s, sms, err);
+  const int shape =
+      a.M <= 128 ? 128 : large_shape(a.M, a.N, (a.K + kStageK - 1) / kStageK, sms);
+  if (shape == 128) return launch<FMT, 128>(xcodes, wcodes, a, static_w, s, sms, err);
+  if (shape == 256) return launch_pair<FMT, 256>(xcodes, wcodes, a, static_w, s, sms, err);
+  return launch_pair<FMT, 384>(xcodes, wcodes, a, static_w, s, sms, err);
 }
 
 }  // namespace

@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(kQuantThreads)
     fp4_quantize_mx_kernel(const __nv_bfloat16* __restrict__ x, int64_t pieces, int per_row,
                            int64_t ldx, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                            __nv_bfloat16* __restrict__ values) {
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kQuantThreads;
   // Whole warps stay in the loop for the shuffles; pieces is a multiple of 8.
@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kQuantThreads)
                            int64_t ldx, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                            float* __restrict__ row_scale, __nv_bfloat16* __restrict__ values) {
   __shared__ float red[kQuantThreads / 32];
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
   constexpr int kRowsPerCta = kQuantThreads / G;
   const int lane = threadIdx.x & 31;
   const int t = threadIdx.x % G;

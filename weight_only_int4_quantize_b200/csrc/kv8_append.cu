@@ -100,8 +100,8 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int log_warps = c.log_page - 4;  // warps of a unit (page, head, side)
   const int w = warp & ((1 << log_warps) - 1);
   const int64_t unit = (static_cast<int64_t>(blockIdx.x) << (3 - log_warps)) + (warp >> log_warps);
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
   if (unit >= units) return;
   const bool is_v = (unit & 1) != 0;
   const int h = static_cast<int>((unit >> 1) % c.heads);

@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   const int rt = prob % a.row_tiles;
   const int bh = prob / a.row_tiles;
   const int h = bh % a.c.heads, b = bh / a.c.heads;
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
   const Kv8Seq s = kv8_sequence(a.bt, b, a.c.log_page);
   if (s.bad && threadIdx.x == 0 && h == 0 && rt == 0 && rank == 0)
     record_error(err, kErrBadIndex, kKernelIdAttn);
