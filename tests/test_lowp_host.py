@@ -127,23 +127,30 @@ def test_binding_refuses_tensors(lib):
         w4.kv8_attention(q, cache, None, None)
 
 
-def test_rows_of_strides():
-    base = torch.zeros(6, 10, 8)
-    assert w4._rows_of(base, 80, "x") == 80
-    assert w4._rows_of(base[:, 2:5], 24, "x") == 80     # slices of wider rows
-    assert w4._rows_of(base[:1, 2:5], 24, "x") == 24    # one row has no stride
-    for bad in (base[:, :, :4], base.transpose(1, 2), base[:, ::2], base[:1].expand(6, 10, 8)):
+def test_row_strides_refused(lib):
+    """Only the first axis may be strided, and rows may not overlap; what
+    passes these checks is refused for not lying on a GPU."""
+    base = torch.zeros(6, 256, dtype=torch.bfloat16)
+    for ok in (base, base[:, :128], base[:, 128:], base[2:3]):
+        with pytest.raises(TypeError, match="CUDA"):
+            w4.fp4_quantize(ok)
+    for bad in (base.t(), base[:, ::2], base[:1].expand(6, 256)):
         with pytest.raises(ValueError):
-            w4._rows_of(bad, bad[0].numel(), "x")
+            w4.fp4_quantize(bad)
+    with pytest.raises(ValueError):
+        w4.fp4_quantize(base[0])
+    with pytest.raises(TypeError):
+        w4.fp4_quantize(base.float())
 
 
-def test_shape_mismatches_refused(monkeypatch):
+def test_shape_mismatches_refused(lib):
     """The C ABI takes bare pointers: the binding refuses buffers of another
-    size (the library is not reached)."""
-    monkeypatch.setattr(w4, "_cuda", lambda t, dtype, name: t)
-    monkeypatch.setattr(w4, "_cuda_rows", lambda t, dtype, name: t)
+    size before it asks where they lie."""
     u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
     xs, ws = u8(1, 1, 512), u8(2, 1, 512)
+    with pytest.raises(TypeError, match="CUDA"):
+        w4.fp4_linear(u8(4, 64), xs, None, u8(130, 64), ws, None, out=bf(4, 130))
     with pytest.raises(ValueError):
         w4.fp4_linear(u8(4, 64), xs, None, u8(130, 128), ws, None)         # K differs
     with pytest.raises(ValueError):
@@ -154,31 +161,61 @@ def test_shape_mismatches_refused(monkeypatch):
         w4.fp4_linear(u8(4, 64), u8(1, 2, 512), torch.zeros(3), u8(130, 64), u8(2, 2, 512),
                       torch.zeros(130), "nv")
     with pytest.raises(ValueError):
-        w4.fp4_linear(u8(4, 64), xs, None, u8(130, 64), ws, None, out=torch.zeros(4, 131))
+        w4.fp4_linear(u8(4, 64), u8(1, 2, 512), None, u8(130, 64), u8(2, 2, 512), None, "nv")
+    with pytest.raises(ValueError):
+        w4.fp4_linear(u8(4, 64), xs, None, u8(130, 64), ws, None, out=bf(4, 131))
+    with pytest.raises(ValueError):
+        w4.fp4_linear(u8(4, 128)[:, ::2], xs, None, u8(130, 64), ws, None)
+    with pytest.raises(TypeError):
+        w4.fp4_linear(u8(4, 64).char(), xs, None, u8(130, 64), ws, None)
+    with pytest.raises(TypeError):
+        w4.fp4_linear(u8(4, 64), xs, None, u8(130, 64), ws, None, flags="none")
     cache = w4.kv8_cache(4, 2, 16, 64, device="cpu")
     table, lens = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
-    starts = torch.zeros(4, dtype=torch.int32)
-    k = torch.zeros(5, 2, 64)
-    with pytest.raises(ValueError):
-        w4.kv8_append(cache, k, k, table, lens, starts)                    # max_new missing
-    with pytest.raises(ValueError):
-        w4.kv8_append(cache, k, k, table, lens, starts[:3], 2)
-    with pytest.raises(ValueError):
-        w4.kv8_append(cache, k, k, table, lens[:2], starts, 2)
+    starts, k = torch.zeros(4, dtype=torch.int32), bf(5, 2, 64)
+    for f in (lambda c=cache, x=k, *a: w4.kv8_append(c, x, x, *a),
+              lambda c=cache, x=k, *a: w4.kv8_attention(x, c, *a)):
+        with pytest.raises(TypeError, match="CUDA"):
+            f(cache, k, table, lens, starts, 2)
+        with pytest.raises(ValueError):
+            f(cache, k, table, lens, starts)                               # max_new missing
+        with pytest.raises(ValueError):
+            f(cache, k, table, lens, starts[:3], 2)
+        with pytest.raises(ValueError):
+            f(cache, k, table, lens[:2], starts, 2)
+        with pytest.raises(ValueError):
+            f(cache, k, table[0], lens, starts, 2)
+        with pytest.raises(ValueError):
+            f(cache, k, table, lens, None, 2)
+        with pytest.raises(TypeError):
+            f(cache, k, table.long(), lens, starts, 2)
+        with pytest.raises(TypeError):
+            f(cache, k.float(), table, lens, starts, 2)
+        with pytest.raises(ValueError):
+            f(cache, k[:, :, :32], table, lens, starts, 2)
+        with pytest.raises(ValueError):
+            f(cache._replace(v_codes=cache.k_codes), k, table, lens, starts, 2)
+        with pytest.raises(ValueError):
+            f(cache._replace(k_scales=cache.k_scales[:3]), k, table, lens, starts, 2)
+        with pytest.raises(TypeError):
+            f(cache._replace(k_codes=cache.k_codes.float()), k, table, lens, starts, 2)
+        with pytest.raises(TypeError):
+            f(list(cache), k, table, lens, starts, 2)
     with pytest.raises(ValueError):
         w4.kv8_append(cache, k, k[:4], table, lens, starts, 2)
     with pytest.raises(ValueError):
         w4.kv8_append(cache, k[:, :1], k[:, :1], table, lens, starts, 2)
     with pytest.raises(ValueError):
-        w4.kv8_append(cache, k, k, table, lens, None, 2)
-    with pytest.raises(ValueError):
-        w4.kv8_append(cache._replace(v_codes=cache.k_codes), k, k, table, lens, starts, 2)
-    with pytest.raises(ValueError):
-        w4.kv8_append(cache._replace(k_scales=cache.k_scales[:3]), k, k, table, lens, starts, 2)
-    with pytest.raises(ValueError):
-        w4.kv8_attention(k[:, :, :32], cache, table, lens, starts, 2)
-    with pytest.raises(ValueError):
         w4.kv8_attention(k, cache, table, lens, starts, 2, out=k[:4])
+
+
+def test_missing_extension_fails_loudly(lib, monkeypatch):
+    import sys
+    monkeypatch.setattr(w4, "_TENSORS", None)
+    monkeypatch.delattr(w4, "_tensors", raising=False)
+    monkeypatch.setitem(sys.modules, w4.__name__ + "._tensors", None)
+    with pytest.raises(RuntimeError, match="no fallback"):
+        w4.fp4_quantize(torch.zeros(1, 128, dtype=torch.bfloat16))
 
 
 # ----------------------------------------------------------- oracle pins ----

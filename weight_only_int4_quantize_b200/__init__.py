@@ -695,52 +695,30 @@ def fp4_scale_shape(rows: int, k: int, fmt: str):
     return ((rows + 127) // 128, k // (4 * block), 512)
 
 
-# The operators below are called once per linear or layer of a decode step, so
-# the binding's own time counts: it asks torch for plain integers (device
-# index, raw stream) and enters a device context only where the tensors' is
-# not the current one.
+# The four operators below are called once per linear or layer of a decode
+# step: their checks, allocations and calls into libw4 run in the _tensors
+# extension (csrc/tensors.cpp), a few microseconds per call.
+
+_TENSORS = None
 
 
-def _call(fn, where, index, args):
-    """fn(*args, current stream of device `index`) with that device current."""
-    torch = _torch()
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch._C._cuda_getDevice() == index:
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, stream)
-    if st != 0:
-        raise W4Error(st, where)
-
-
-def _on_device(t, index, name):
-    if t is not None and t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{index}")
-
-
-def _rows_of(t, width, name):
-    """Elements between the rows of a tensor whose rows (everything but the
-    first axis) are contiguous: slices of a wider buffer's rows are allowed."""
-    if t.is_contiguous():
-        return width
-    inner = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != inner:
-            raise ValueError(f"{name}: only the first axis may be strided")
-        inner *= size
-    if t.shape[0] > 1 and t.stride(0) < width:
-        raise ValueError(f"{name}: rows overlap")
-    return t.stride(0) if t.shape[0] > 1 else width
-
-
-def _cuda_rows(t, dtype, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t
+def _front_end():
+    """The extension, initialized with libw4's entry points (raises if either
+    has not been built)."""
+    global _TENSORS
+    if _TENSORS is None:
+        L = lib()
+        try:
+            from . import _tensors as ext
+        except ImportError as e:
+            raise RuntimeError(
+                "the _tensors extension is missing: build it with "
+                "`python -m weight_only_int4_quantize_b200.build` (no fallback exists)") from e
+        ext.init(*[ctypes.cast(f, ctypes.c_void_p).value for f in
+                   (L.w4_fp4_quantize, L.w4_fp4_linear, L.w4_kv8_append, L.w4_kv8_attention)],
+                 W4Error)
+        _TENSORS = ext
+    return _TENSORS
 
 
 def fp4_quantize(x, fmt: str = "mx", values: bool = False):
@@ -750,61 +728,15 @@ def fp4_quantize(x, fmt: str = "mx", values: bool = False):
     Returns (codes uint8 [R, K/2], scale tiles uint8 [ceil(R/128), blocks/4,
     512], row scales float32 [R] or None for "mx"), and with values=True also
     the bf16 [R, K] values that the codes stand for."""
-    torch = _torch()
-    f, block = _fp4_format(fmt)
-    _cuda_rows(x, torch.bfloat16, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [R, K]")
-    r, k = x.shape
-    ldx = _rows_of(x, k, "x")
-    codes = x.new_empty((r, k // 2), dtype=torch.uint8)
-    scales = x.new_empty(((r + 127) // 128, k // (4 * block), 512), dtype=torch.uint8)
-    row = x.new_empty((r,), dtype=torch.float32) if f == 1 else None
-    val = x.new_empty((r, k)) if values else None
-    _call(lib().w4_fp4_quantize, "w4_fp4_quantize", x.get_device(),
-          (x.data_ptr(), r, k, ldx, f, codes.data_ptr(), scales.data_ptr(),
-           None if row is None else row.data_ptr(), None if val is None else val.data_ptr()))
-    return (codes, scales, row, val) if values else (codes, scales, row)
+    return (_TENSORS or _front_end()).fp4_quantize(x, fmt, values)
 
 
 def fp4_linear(xcodes, xscales, xrow, wcodes, wscales, wrow, fmt: str = "mx", flags: int = 0,
                out=None):
     """y = x . w^T, bf16 [M, N], of an activation and a weight in the same
     microscaled 4-bit format (each as fp4_quantize returns it)."""
-    torch = _torch()
-    f, block = _fp4_format(fmt)
-    u8 = torch.uint8
-    _cuda(xcodes, u8, "xcodes")
-    _cuda(xscales, u8, "xscales")
-    _cuda(wcodes, u8, "wcodes")
-    _cuda(wscales, u8, "wscales")
-    if xcodes.dim() != 2 or wcodes.dim() != 2:
-        raise ValueError("xcodes and wcodes must be [rows, K/2]")
-    m, k2 = xcodes.shape
-    k, n, tiles = 2 * k2, wcodes.shape[0], 2 * k2 // (4 * block)
-    _expect(wcodes, (n, k2), "wcodes")
-    _expect(xscales, ((m + 127) // 128, tiles, 512), "xscales")
-    _expect(wscales, ((n + 127) // 128, tiles, 512), "wscales")
-    if (xrow is None) != (f == 0) or (wrow is None) != (f == 0):
-        raise ValueError("xrow and wrow belong to format 'nv' alone")
-    if f == 1:
-        _cuda(xrow, torch.float32, "xrow")
-        _cuda(wrow, torch.float32, "wrow")
-        _expect(xrow, (m,), "xrow")
-        _expect(wrow, (n,), "wrow")
-    if out is not None:
-        _cuda(out, torch.bfloat16, "out")
-        _expect(out, (m, n), "out")
-    at = xcodes.get_device()
-    for t, name in ((xscales, "xscales"), (wcodes, "wcodes"), (wscales, "wscales"),
-                    (xrow, "xrow"), (wrow, "wrow"), (out, "out")):
-        _on_device(t, at, name)
-    y = out if out is not None else xcodes.new_empty((m, n), dtype=torch.bfloat16)
-    _call(lib().w4_fp4_linear, "w4_fp4_linear", at,
-          (xcodes.data_ptr(), xscales.data_ptr(), None if xrow is None else xrow.data_ptr(), m,
-           wcodes.data_ptr(), wscales.data_ptr(), None if wrow is None else wrow.data_ptr(), n, k,
-           f, y.data_ptr(), int(flags)))
-    return y
+    return (_TENSORS or _front_end()).fp4_linear(xcodes, xscales, xrow, wcodes, wscales, wrow, fmt,
+                                               flags, out)
 
 
 class KV8Cache(NamedTuple):
@@ -818,6 +750,7 @@ class KV8Cache(NamedTuple):
 
 
 class _KV8Cache(ctypes.Structure):
+    """w4_kv8_cache, for callers of the C ABI."""
     _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
                 ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
@@ -839,68 +772,12 @@ def kv8_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, dtyp
     return KV8Cache(k.view(dtype), v.view(dtype), *s)
 
 
-def _kv8_args(ref, cache, page_table, seq_lens, starts, max_new):
-    """Checks of what appending and attention share; ref is [rows, heads,
-    head_dim].  Returns the C cache, the batch size and max_new."""
-    torch = _torch()
-    k, v, ks, vs = cache
-    if not isinstance(k, torch.Tensor) or k.dtype not in (torch.int8, torch.float8_e4m3fn):
-        raise TypeError("cache codes must be int8 or float8_e4m3fn")
-    dt = k.dtype
-    _cuda(k, dt, "k_codes")
-    _cuda(v, dt, "v_codes")
-    _cuda(ks, torch.float32, "k_scales")
-    _cuda(vs, torch.float32, "v_scales")
-    _cuda(page_table, torch.int32, "page_table")
-    _cuda(seq_lens, torch.int32, "seq_lens")
-    if k.dim() != 4:
-        raise ValueError("k_codes must be [pages, kv_heads, page_size, head_dim]")
-    pages, heads, page, d = k.shape
-    _expect(v, (pages, heads, d, page), "v_codes")
-    _expect(ks, (pages, heads), "k_scales")
-    _expect(vs, (pages, heads), "v_scales")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [batch, max_pages]")
-    b = page_table.shape[0]
-    _expect(seq_lens, (b,), "seq_lens")
-    if starts is not None:
-        _cuda(starts, torch.int32, "starts")
-        _expect(starts, (b + 1,), "starts")
-        if max_new is None:
-            raise ValueError("max_new is needed with starts")
-    elif max_new not in (None, 1):
-        raise ValueError("without starts every sequence has one new token")
-    if ref.dim() != 3 or ref.shape[2] != d:
-        raise ValueError(f"new tokens must be [rows, heads, {d}]")
-    at = ref.get_device()
-    for t, name in ((k, "k_codes"), (v, "v_codes"), (ks, "k_scales"), (vs, "v_scales"),
-                    (page_table, "page_table"), (seq_lens, "seq_lens"), (starts, "starts")):
-        _on_device(t, at, name)
-    c = _KV8Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, heads, page, d,
-                  0 if dt == torch.int8 else 1)
-    return c, b, 1 if max_new is None else int(max_new)
-
-
 def kv8_append(cache, k, v, page_table, seq_lens, starts=None, max_new=None) -> None:
     """Writes new keys and values (bf16 [rows, kv_heads, head_dim]; only the
     token axis may be strided) into the cache's pages.  seq_lens int32 [batch]
     counts the new tokens; starts int32 [batch + 1] gives each sequence's rows
     (with max_new, at least the most of any), None one token each."""
-    torch = _torch()
-    _cuda_rows(k, torch.bfloat16, "k")
-    _cuda_rows(v, torch.bfloat16, "v")
-    c, b, most = _kv8_args(k, cache, page_table, seq_lens, starts, max_new)
-    rows, heads, d = k.shape
-    if heads != c.kv_heads:
-        raise ValueError(f"k has {heads} heads, the cache {c.kv_heads}")
-    _expect(v, (rows, heads, d), "v")
-    at = k.get_device()
-    _on_device(v, at, "v")
-    ldk, ldv = _rows_of(k, heads * d, "k"), _rows_of(v, heads * d, "v")
-    _call(lib().w4_kv8_append, "w4_kv8_append", at,
-          (ctypes.byref(c), k.data_ptr(), ldk, v.data_ptr(), ldv, rows, page_table.data_ptr(),
-           page_table.shape[1], seq_lens.data_ptr(), None if starts is None else starts.data_ptr(),
-           b, most))
+    (_TENSORS or _front_end()).kv8_append(cache, k, v, page_table, seq_lens, starts, max_new)
 
 
 def kv8_attention(q, cache, page_table, seq_lens, starts=None, max_new=None, scale=None, out=None):
@@ -909,22 +786,8 @@ def kv8_attention(q, cache, page_table, seq_lens, starts=None, max_new=None, sca
     already; other arguments as kv8_append.  scale: 1/sqrt(head_dim) if None.
     Returns bf16 [rows, q_heads, head_dim]; rows of no sequence are not
     written."""
-    torch = _torch()
-    _cuda_rows(q, torch.bfloat16, "q")
-    c, b, most = _kv8_args(q, cache, page_table, seq_lens, starts, max_new)
-    rows, heads, d = q.shape
-    ldq = _rows_of(q, heads * d, "q")
-    at = q.get_device()
-    if out is not None:
-        _cuda(out, torch.bfloat16, "out")
-        _expect(out, (rows, heads, d), "out")
-        _on_device(out, at, "out")
-    o = out if out is not None else q.new_empty((rows, heads, d))
-    _call(lib().w4_kv8_attention, "w4_kv8_attention", at,
-          (q.data_ptr(), ldq, rows, heads, ctypes.byref(c), page_table.data_ptr(),
-           page_table.shape[1], seq_lens.data_ptr(), None if starts is None else starts.data_ptr(),
-           b, most, float(d ** -0.5 if scale is None else scale), o.data_ptr()))
-    return o
+    return (_TENSORS or _front_end()).kv8_attention(q, cache, page_table, seq_lens, starts, max_new,
+                                                  scale, out)
 
 
 def device_error(clear: bool = True) -> int:

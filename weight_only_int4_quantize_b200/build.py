@@ -1,4 +1,6 @@
-"""Builds libw4.so in-tree with nvcc for sm_100a (no GPU needed to compile).
+"""Builds libw4.so in-tree with nvcc for sm_100a (no GPU needed to compile),
+and the _tensors extension (the tensor front end of the per-layer operators)
+with the C++ compiler against torch's headers.
 
     python -m weight_only_int4_quantize_b200.build [--verbose]
 
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libw4.so")
+TENSORS = os.path.join(PKG, "_tensors" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["abi.cu", "quantize.cu", "gemv.cu", "gemv_stream.cu", "act_int8.cu", "gemm_tc.cu", "awq.cu", "block.cu", "noalloc.cu",
            "fp4_quant.cu", "fp4_gemm.cu", "kv8_append.cu", "kv8_attn.cu"]
@@ -34,7 +38,8 @@ def _nvcc() -> str:
 
 
 def _deps_mtime() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "w4.h")]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "tensors.cpp"]
+    files.append(os.path.join(INCLUDE, "w4.h"))
     return max(os.path.getmtime(f) for f in files)
 
 
@@ -58,7 +63,29 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+    build_tensors(verbose)
     return LIB
+
+
+def build_tensors(verbose: bool = False) -> str:
+    """Compiles csrc/tensors.cpp into the package's _tensors module."""
+    import torch
+    from torch.utils import cpp_extension
+    src = os.path.join(CSRC, "tensors.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "w4.h"), torch.__file__))
+    if os.path.exists(TENSORS) and os.path.getmtime(TENSORS) >= newest:
+        return TENSORS
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           f"-isystem{sysconfig.get_paths()['include']}", f"-isystem{cuda}/include",
+           *[f"-isystem{p}" for p in cpp_extension.include_paths()], src,
+           *[f"-L{p}" for p in cpp_extension.library_paths()], "-ltorch_python", "-ltorch_cuda",
+           "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10", "-o", TENSORS]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return TENSORS
 
 
 if __name__ == "__main__":
