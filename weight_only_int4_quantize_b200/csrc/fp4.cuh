@@ -43,16 +43,17 @@ __device__ __forceinline__ __half2 e2m1_pair_to_f16(uint32_t c, int i) {
   return __hmul2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x7400)));
 }
 
-// Nearest e4m3 code of v >= 0 (ties to even, at most 448), and its value.
+// Nearest e4m3 code of 0 <= v <= 448 (ties to even), and a code's value.
+// v 2^-120 has e4m3's exponent field (subnormals included) as its own, so the
+// code is its bits rounded to the top three of the mantissa.  Integer
+// arithmetic: the conversion instructions share the pipe that the e2m1
+// conversions fill.
 __device__ __forceinline__ uint32_t e4m3_of(float v) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
-  return r & 0xFFu;
+  const uint32_t b = __float_as_uint(v * 0x1p-120f);
+  return (b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20;
 }
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code)));
-  return __half2float(__ushort_as_half(static_cast<uint16_t>(h & 0xFFFFu)));
+  return __uint_as_float(code << 20) * 0x1p120f;
 }
 
 // 2^e for -149 <= e <= 127 (subnormal results included).

@@ -12,18 +12,19 @@
 // Every decision is taken on exact values.  mx: x 2^-e is exact.  nv: 6 t
 // for an e4m3 rounding border t has 7 significant bits, and b s for an e2m1
 // border b has 7, while x has 8: a quotient that is not on its border is at
-// least 2^-9 (relative) away from it.  So the correctly rounded amax / 6
-// decides the scale exactly, and x * rcp(s), off by at most 2^-21, decides
-// the code exactly once it is rounded to 13 significant bits, which puts the
-// quotients that lie on a border back on it.  The values (2 + 4 significant
+// least 2^-9 (relative) away from it.  So the products amax * (1 / 6) and x * (1 / s),
+// with factors a little large (by 2^-20, more than all their rounding errors
+// together) and cut to 13 significant bits, lie on the side of every border
+// that the true quotient lies on, and on it where that does.  The values (2 + 4 significant
 // bits, or 2) are exact in bf16 from 2^-126 up.
 //
 // Bound: HBM (2 bytes read and 0.53 / 0.56 written per weight, 2 more with
 // values).  A thread owns 16 consecutive channels; the largest magnitude of
 // an mx block takes one shuffle, of an nv block none.  The four scale bytes
 // of a tile word are gathered by shuffles and stored as one word.  The nv
-// row maximum is a first pass over the row, which stays in registers up to
-// 64 channels per thread.
+// row maximum is a first pass over the row, which stays in registers: a row's
+// CTA has as many warps as it takes at one or two pieces per thread (8192 x
+// 17408: 140 us with 256 threads whatever the row, 4 or 5 pieces each).
 #include "fp4.cuh"
 #include "w4_kernels.h"
 
@@ -32,8 +33,6 @@ namespace w4 {
 namespace {
 
 constexpr int kQuantThreads = 256;
-constexpr int kHeld = 4;  // 16-channel pieces a thread keeps in registers between the nv passes
-
 struct Piece {
   uint32_t u[8];  // 16 bf16
 };
@@ -72,6 +71,20 @@ __device__ __forceinline__ void scaled(const Piece& p, float pow2, float (&v)[16
     v[2 * i] = __uint_as_float(u << 16);
     v[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
   }
+}
+
+// v cut to 13 significant bits (towards zero).
+__device__ __forceinline__ float cut(float v) {
+  return __uint_as_float(__float_as_uint(v) & 0xFFFFF800u);
+}
+
+// 1 / 6 and 1 / s (s normal), 2^-20 large: the approximate reciprocal is off
+// by at most one unit in the last place, the products by half of one each.
+constexpr float kSixth = 0.16666666666f * (1.f + 0x1p-20f);
+__device__ __forceinline__ float reciprocal_up(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r * (1.f + 0x1p-20f);
 }
 
 __device__ __forceinline__ uint2 codes_of(const float (&v)[16]) {
@@ -145,88 +158,107 @@ __global__ void __launch_bounds__(kQuantThreads)
   }
 }
 
-// nv: G threads (a warp or the CTA) own one row at a time.
-template <bool VALUES, int G>
-__global__ void __launch_bounds__(kQuantThreads)
+// nv: a warp (WARP) or the CTA owns one row; a thread keeps HELD pieces in
+// registers between the passes (the rest of a longer row is read again).
+template <bool VALUES, bool WARP, int HELD>
+__global__ void __maxnreg__(HELD == 1 ? 48 : 64)
     fp4_quantize_nv_kernel(const __nv_bfloat16* __restrict__ x, int64_t rows, int per_row,
                            int64_t ldx, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                            float* __restrict__ row_scale, __nv_bfloat16* __restrict__ values) {
-  __shared__ float red[kQuantThreads / 32];
+  __shared__ float red[2][32];
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int kRowsPerCta = kQuantThreads / G;
   const int lane = threadIdx.x & 31;
-  const int t = threadIdx.x % G;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + threadIdx.x / G;
-  if (G == 32 && row >= rows) return;  // whole warps; with G = 256 every CTA has a row
-  const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
+  const int G = WARP ? 32 : static_cast<int>(blockDim.x);
+  const int t = WARP ? lane : static_cast<int>(threadIdx.x);
+  const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32) : gridDim.x;
+  int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5)
+                     : static_cast<int64_t>(blockIdx.x);
 
-  Piece held[kHeld];
-  float amax = 0.f;
+  // The next row is on its way while this one is reduced and written.
+  Piece next[HELD];
+  auto fetch = [&](int64_t at) {
+    const uint4* xr = reinterpret_cast<const uint4*>(x + at * ldx);
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    const int c = t + j * G;
-    held[j] = Piece{};
-    if (c < per_row) held[j] = load_piece(xr + 2 * c);
-  }
-#pragma unroll
-  for (int j = 0; j < kHeld; ++j) amax = fmaxf(amax, piece_amax(held[j]));
-  for (int c = t + kHeld * G; c < per_row; c += G)
-    amax = fmaxf(amax, piece_amax(load_piece(xr + 2 * c)));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (G > 32) {
-    if (lane == 0) red[threadIdx.x >> 5] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kQuantThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-  }
-  // amax = f 2^n with 1 <= f < 2, and 2688 = 1.3125 * 2^11.
-  int E = 0;
-  if (amax > 0.f) {
-    const uint32_t u = __float_as_uint(amax);
-    E = static_cast<int>(u >> 23) - 127 - ((u & 0x7FFFFFu) <= 0x280000u ? 11 : 10);
-    if (E < -126) E = -126;  // also every subnormal maximum
-  }
-  const float up = exp2_int(E), down = exp2_int(-E);
-  if (t == 0) row_scale[row] = up;
-
-  const int64_t words = per_row >> 2;
-  auto emit = [&](int c, const Piece& p) {
-    // Called by whole groups of 4 lanes (per_row is a multiple of 8).
-    const float top = piece_amax(p) * down;
-    const uint32_t byte = e4m3_of(__fdiv_rn(top, 6.0f));
-    const float s = e4m3_value(byte);
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-    float v[16];
-    scaled(p, down, v);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)  // 13 significant bits
-      v[i] = __uint_as_float((__float_as_uint(v[i] * r) + 0x400u) & 0xFFFFF800u);
-    const uint2 q = codes_of(v);
-    const uint32_t four = 0xFu << (lane & ~3);
-    const uint32_t b1 = __shfl_down_sync(four, byte, 1, 4);
-    const uint32_t b2 = __shfl_down_sync(four, byte, 2, 4);
-    const uint32_t b3 = __shfl_down_sync(four, byte, 3, 4);
-    const int64_t i = row * per_row + c;
-    reinterpret_cast<uint2*>(codes)[i] = q;
-    if ((lane & 3) == 0)
-      *scale_word(scales, row, c >> 2, words) = byte | (b1 << 8) | (b2 << 16) | (b3 << 24);
-    if (VALUES) store_values(q, s * up, reinterpret_cast<uint4*>(values) + 2 * i);
+    for (int j = 0; j < HELD; ++j) {
+      const int c = t + j * G;
+      next[j] = Piece{};
+      if (at < rows && c < per_row) next[j] = load_piece(xr + 2 * c);
+    }
   };
+  fetch(row);
+  for (int turn = 0; row < rows; row += step, turn ^= 1) {
+    const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
+    Piece held[HELD];
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    const int c = t + j * G;
-    if (c < per_row) emit(c, held[j]);
+    for (int j = 0; j < HELD; ++j) held[j] = next[j];
+    fetch(row + step);
+    float amax = 0.f, top[HELD];
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      top[j] = piece_amax(held[j]);
+      amax = fmaxf(amax, top[j]);
+    }
+    for (int c = t + HELD * G; c < per_row; c += G)
+      amax = fmaxf(amax, piece_amax(load_piece(xr + 2 * c)));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (!WARP) {
+      // Two sets of maxima in turn: a warp may be a row ahead, not two.
+      if (lane == 0) red[turn][threadIdx.x >> 5] = amax;
+      __syncthreads();
+      amax = lane < (G >> 5) ? red[turn][lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    }
+    // amax = f 2^n with 1 <= f < 2, and 2688 = 1.3125 * 2^11.
+    int E = 0;
+    if (amax > 0.f) {
+      const uint32_t u = __float_as_uint(amax);
+      E = static_cast<int>(u >> 23) - 127 - ((u & 0x7FFFFFu) <= 0x280000u ? 11 : 10);
+      if (E < -126) E = -126;  // also every subnormal maximum
+    }
+    const float up = exp2_int(E), down = exp2_int(-E);
+    if (t == 0) row_scale[row] = up;
+
+    const int64_t words = per_row >> 2;
+    auto emit = [&](int c, const Piece& p, float largest) {
+      // Called by whole groups of 4 lanes (per_row is a multiple of 8).
+      const uint32_t byte = e4m3_of(cut(largest * down * kSixth));
+      const float s = e4m3_value(byte);
+      const float r = s > 0.f ? reciprocal_up(s) : 0.f;
+      float v[16];
+      scaled(p, down, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = cut(v[i] * r);
+      const uint2 q = codes_of(v);
+      const uint32_t four = 0xFu << (lane & ~3);
+      const uint32_t b1 = __shfl_down_sync(four, byte, 1, 4);
+      const uint32_t b2 = __shfl_down_sync(four, byte, 2, 4);
+      const uint32_t b3 = __shfl_down_sync(four, byte, 3, 4);
+      const int64_t i = row * per_row + c;
+      reinterpret_cast<uint2*>(codes)[i] = q;
+      if ((lane & 3) == 0)
+        *scale_word(scales, row, c >> 2, words) = byte | (b1 << 8) | (b2 << 16) | (b3 << 24);
+      if (VALUES) store_values(q, s * up, reinterpret_cast<uint4*>(values) + 2 * i);
+    };
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      const int c = t + j * G;
+      if (c < per_row) emit(c, held[j], top[j]);
+    }
+    for (int c = t + HELD * G; c < per_row; c += G) {
+      const Piece p = load_piece(xr + 2 * c);
+      emit(c, p, piece_amax(p));
+    }
   }
-  for (int c = t + kHeld * G; c < per_row; c += G) emit(c, load_piece(xr + 2 * c));
 }
 
 template <auto kern, typename... Args>
-cudaError_t launch_pdl(int64_t grid, cudaStream_t stream, Args... args) {
+cudaError_t launch_pdl(int64_t grid, int threads, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kQuantThreads, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -236,6 +268,37 @@ cudaError_t launch_pdl(int64_t grid, cudaStream_t stream, Args... args) {
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+template <bool VALUES>
+cudaError_t quantize(const __nv_bfloat16* x, int64_t R, int64_t K, int64_t ldx, int fmt,
+                     uint8_t* codes, uint8_t* scales, float* row_scale, __nv_bfloat16* values,
+                     cudaStream_t stream, int num_sms) {
+  const int per_row = static_cast<int>(K / 16);
+  if (fmt == kFp4Mx) {
+    const int64_t pieces = R * per_row;
+    const int64_t want = (pieces + kQuantThreads - 1) / kQuantThreads;
+    const int64_t grid = want < int64_t{num_sms} * 64 ? want : int64_t{num_sms} * 64;
+    return launch_pdl<fp4_quantize_mx_kernel<VALUES>>(grid, kQuantThreads, stream, x, pieces,
+                                                      per_row, ldx, codes, scales, values);
+  }
+  if (per_row <= 64) {
+    const int64_t want = (R + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
+    const int64_t grid = want < int64_t{num_sms} * 4 ? want : int64_t{num_sms} * 4;
+    return launch_pdl<fp4_quantize_nv_kernel<VALUES, true, 2>>(
+        grid, kQuantThreads, stream, x, R, per_row, ldx, codes, scales, row_scale, values);
+  }
+  // One piece per thread up to 512 threads (few rows: the latency of one
+  // round), then two; as many CTAs as are resident at once.
+  const int pieces = per_row <= 512 ? per_row : (per_row + 1) / 2;
+  const int threads = pieces < 1024 ? (pieces + 31) & ~31 : 1024;
+  const int64_t most = int64_t{num_sms} * (65536 / ((per_row <= 512 ? 48 : 64) * threads));
+  const int64_t grid = R < most ? R : most;
+  return per_row <= 512
+             ? launch_pdl<fp4_quantize_nv_kernel<VALUES, false, 1>>(
+                   grid, threads, stream, x, R, per_row, ldx, codes, scales, row_scale, values)
+             : launch_pdl<fp4_quantize_nv_kernel<VALUES, false, 2>>(
+                   grid, threads, stream, x, R, per_row, ldx, codes, scales, row_scale, values);
+}
+
 }  // namespace
 
 cudaError_t launch_fp4_quantize(const void* x, int64_t R, int64_t K, int64_t ldx, int fmt,
@@ -243,27 +306,8 @@ cudaError_t launch_fp4_quantize(const void* x, int64_t R, int64_t K, int64_t ldx
                                 cudaStream_t stream, int num_sms) {
   const auto* xp = static_cast<const __nv_bfloat16*>(x);
   auto* vp = static_cast<__nv_bfloat16*>(values);
-  const int per_row = static_cast<int>(K / 16);
-  if (fmt == kFp4Mx) {
-    const int64_t pieces = R * per_row;
-    const int64_t want = (pieces + kQuantThreads - 1) / kQuantThreads;
-    const int64_t grid = want < int64_t{num_sms} * 64 ? want : int64_t{num_sms} * 64;
-    return vp ? launch_pdl<fp4_quantize_mx_kernel<true>>(grid, stream, xp, pieces, per_row, ldx,
-                                                         codes, scales, vp)
-              : launch_pdl<fp4_quantize_mx_kernel<false>>(grid, stream, xp, pieces, per_row, ldx,
-                                                          codes, scales, vp);
-  }
-  if (K <= 1024) {
-    const int64_t grid = (R + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
-    return vp ? launch_pdl<fp4_quantize_nv_kernel<true, 32>>(grid, stream, xp, R, per_row, ldx,
-                                                             codes, scales, row_scale, vp)
-              : launch_pdl<fp4_quantize_nv_kernel<false, 32>>(grid, stream, xp, R, per_row, ldx,
-                                                              codes, scales, row_scale, vp);
-  }
-  return vp ? launch_pdl<fp4_quantize_nv_kernel<true, kQuantThreads>>(
-                  R, stream, xp, R, per_row, ldx, codes, scales, row_scale, vp)
-            : launch_pdl<fp4_quantize_nv_kernel<false, kQuantThreads>>(
-                  R, stream, xp, R, per_row, ldx, codes, scales, row_scale, vp);
+  return vp ? quantize<true>(xp, R, K, ldx, fmt, codes, scales, row_scale, vp, stream, num_sms)
+            : quantize<false>(xp, R, K, ldx, fmt, codes, scales, row_scale, vp, stream, num_sms);
 }
 
 }  // namespace w4

@@ -90,7 +90,7 @@ __device__ __forceinline__ uint32_t byte_mask(int first, int lo, int hi) {
 }
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 4)
     kv8_append_kernel(const Kv8Cache c, const Kv8Batch bt, const __nv_bfloat16* __restrict__ k,
                       const __nv_bfloat16* __restrict__ v, int64_t ldk, int64_t ldv, int touched,
                       int64_t units, unsigned* err) {
@@ -119,21 +119,13 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int lo = old > p0 ? static_cast<int>(old - p0) : 0;  // new tokens [lo, hi) of the page
   const int hi = s.len - p0 < page_size ? static_cast<int>(s.len - p0) : page_size;
   const int page = __ldg(bt.table + static_cast<int64_t>(b) * bt.max_pages + j);
-  if (page < 0 || page >= c.num_pages) {
-    if (lane == 0) record_error(err, kErrBadIndex, kKernelIdAppend);
-    return;
-  }
   const int t0 = kGranule * w;  // this warp's tokens of the page
   const int64_t ld = is_v ? ldv : ldk;
-  // Row of token t0 (only those of new tokens are read).
+  // Row of token t0 (only those of new tokens are read).  The rows are on
+  // their way while the page id is.
   const __nv_bfloat16* x = (is_v ? v : k) + static_cast<int64_t>(h) * D + lane * CH +
                            (static_cast<int64_t>(s.row0) + skip + (p0 + t0 - old)) * ld;
-  const int64_t slot = static_cast<int64_t>(page) * c.heads + h;
-  float* scale = (is_v ? c.vs : c.ks) + slot;
-  const float s0 = lo > 0 ? *scale : 0.f;
-
   uint32_t raw[kGranule][CH / 2];
-  uint32_t big = 0;
 #pragma unroll
   for (int t = 0; t < kGranule; ++t) {
 #pragma unroll
@@ -147,9 +139,19 @@ __global__ void __launch_bounds__(kAppendThreads)
         raw[t][0] = __ldg(reinterpret_cast<const uint32_t*>(x + t * ld));
       }
     }
+  }
+  if (page < 0 || page >= c.num_pages) {
+    if (lane == 0) record_error(err, kErrBadIndex, kKernelIdAppend);
+    return;
+  }
+  const int64_t slot = static_cast<int64_t>(page) * c.heads + h;
+  float* scale = (is_v ? c.vs : c.ks) + slot;
+  const float s0 = lo > 0 ? *scale : 0.f;
+  uint32_t big = 0;
+#pragma unroll
+  for (int t = 0; t < kGranule; ++t)
 #pragma unroll
     for (int i = 0; i < CH / 2; ++i) big = __vmaxu2(big, raw[t][i] & 0x7FFF7FFFu);
-  }
   big = max(big & 0xFFFFu, big >> 16);
   big = __reduce_max_sync(0xffffffffu, big);
   if (log_warps > 0) {
@@ -177,10 +179,25 @@ __global__ void __launch_bounds__(kAppendThreads)
     return snap(__uint_as_float((i & 1) ? (u & 0xFFFF0000u) : (u << 16)) * inv);
   };
   if (is_v) {
+    uint8_t* col = c.v + ((slot * D + lane * CH) << c.log_page) + t0;
     const bool whole = t0 >= lo && t0 + kGranule <= hi;
+    const int first = lo > t0 ? lo - t0 : 0, last = hi - t0 < kGranule ? hi - t0 : kGranule;
+    if (!whole && !again && last - first <= 4) {
+      // A few new tokens (a decode step's one): their bytes alone, so that
+      // nothing of the page has to be fetched first.
+#pragma unroll
+      for (int t = 0; t < kGranule; ++t)
+        if (t >= first && t < last) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+            col[(i << c.log_page) + t] =
+                static_cast<uint8_t>(kv_codes<FMT>(value(t, i), 0.f, 0.f, 0.f));
+        }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      uint4* dst = reinterpret_cast<uint4*>(c.v + ((slot * D + lane * CH + i) << c.log_page) + t0);
+      uint4* dst = reinterpret_cast<uint4*>(col + (i << c.log_page));
       uint32_t o[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
