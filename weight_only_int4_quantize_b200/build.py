@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libw4.so")
 TENSORS = os.path.join(PKG, "_tensors" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["abi.cu", "quantize.cu", "gemv.cu", "gemv_stream.cu", "act_int8.cu", "gemm_tc.cu", "awq.cu", "block.cu", "noalloc.cu",
-           "fp4_quant.cu", "fp4_gemm.cu", "kv8_append.cu", "kv8_attn.cu"]
+           "fp4_quant.cu", "fp4_gemm.cu", "kv8_append.cu", "kv8_attn.cu", "kv8_attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

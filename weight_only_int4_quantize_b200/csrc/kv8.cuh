@@ -20,6 +20,27 @@ constexpr unsigned kErrBadIndex = 2u;
 
 __host__ __device__ constexpr float kv8_qmax(int fmt) { return fmt == kKvInt8 ? 127.f : 448.f; }
 
+// Four codes -> two packed pairs of fp16 values.
+template <int FMT>
+__device__ __forceinline__ void kv8_codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == kKvInt8) {
+    // 1024 + (code + 128) has the biased code in its low byte.
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140);
+    const uint32_t b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
 struct Kv8Cache {
   uint8_t* k;
   uint8_t* v;

@@ -40,7 +40,7 @@
 // far and rounded to fp16 with a shift of 2^14 (the largest is 2^14, full
 // precision down to 2^-28 of it); sums and outputs are fp32.
 #include <cooperative_groups.h>
-#include <cuda_fp16.h>
+#include <cstdlib>
 
 #include "kv8.cuh"
 #include "w4_kernels.h"
@@ -95,27 +95,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Four codes -> two packed pairs of fp16 values.
-template <int FMT>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (FMT == kKvInt8) {
-    // 1024 + (code + 128) has the biased code in its low byte.
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140);
-    const uint32_t b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
-  } else {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  }
 }
 
 // Transposes an 8 x 8 matrix of 16-bit values held two per lane.
@@ -325,8 +304,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t f[4];
-            codes_to_f16<FMT>(kw[2 * j][x], f[0], f[2]);
-            codes_to_f16<FMT>(kw[2 * j + 1][x], f[1], f[3]);
+            kv8_codes_to_f16<FMT>(kw[2 * j][x], f[0], f[2]);
+            kv8_codes_to_f16<FMT>(kw[2 * j + 1][x], f[1], f[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(sc[nt][j], f, qb[nt][4 * c + x][0], qb[nt][4 * c + x][1]);
@@ -408,8 +387,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t f[4];
-            codes_to_f16<FMT>(vw[2 * j][x] & mask, f[0], f[2]);
-            codes_to_f16<FMT>(vw[2 * j + 1][x] & mask, f[1], f[3]);
+            kv8_codes_to_f16<FMT>(vw[2 * j][x] & mask, f[0], f[2]);
+            kv8_codes_to_f16<FMT>(vw[2 * j + 1][x] & mask, f[1], f[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(o[nt][j0 + j], f, pb[nt][x][0], pb[nt][x][1]);
@@ -562,6 +541,8 @@ cudaError_t launch_rows(AttnArgs a, cudaStream_t stream, int num_sms, unsigned* 
 cudaError_t launch_kv8_attention(const Kv8Cache& c, const Kv8Batch& bt, const void* q, int64_t ldq,
                                  int q_heads, int D, int fmt, float scale, void* out,
                                  cudaStream_t stream, int num_sms, unsigned* err) {
+  if (getenv("W4_TC") && kv8_attention_tc_fits(c, bt))
+    return launch_kv8_attention_tc(c, bt, q, ldq, q_heads, D, fmt, scale, out, stream, err);
   AttnArgs a;
   a.c = c;
   a.bt = bt;

@@ -1,0 +1,592 @@
+// Causal attention over the 8-bit paged cache (layout: kv8.cuh), tcgen05
+// kernel: long runs of new tokens (prompts and their chunks).
+//
+// One CTA owns 128 rows (row = token * group + head of the group) of one
+// sequence and kv head and walks the keys in tiles of 64:
+//
+//   S = Q K^T            (fp16 operands, fp32 in TMEM)
+//   P = exp2(f S - m)    (fp16 in TMEM, weighted by the value scales)
+//   O += P V             (A operand P from TMEM, fp32 accumulator in TMEM)
+//
+// Warp roles: 0..3 softmax (a thread owns a row), 4 MMA issue, 5..8
+// dequantization: they fetch the codes of the next tile into registers, turn
+// those of this one into fp16 and write the swizzled operand tiles, so codes
+// cross L2 once per 128 rows and never shared memory as bytes.  Two CTAs share
+// an SM, so one's exponentials run under the other's products: per tile the
+// tensor pipe and the exponential unit need 512 cycles each.
+//
+// Numerics as in the rows kernel (kv8_attn.cu): codes are exact in fp16; a
+// query row is scaled by a power of two; key scales (one per 16 keys at the
+// finest) multiply the fp32 scores; value scales weight the probabilities
+// relative to a running reference v_ref.  The running maximum that O is kept
+// relative to is moved only when a row's maximum has grown by more than 2^5,
+// and v_ref only when a value scale exceeds twice it, so O is rescaled in TMEM
+// rarely; P is at most 2^9 * 2^5 * 2 = 2^15 (fp16), full precision from 2^-14.
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "kv8.cuh"
+#include "w4_kernels.h"
+
+namespace w4 {
+
+namespace {
+
+constexpr int kTcThreads = 288;
+constexpr int kTcRows = 128;
+constexpr int kKeys = 64;            // keys of a tile
+constexpr float kTcShift = 9.f;      // probabilities are kept times 2^9
+constexpr float kTcGrow = 5.f;       // the maximum moves once a row's has grown by 2^5
+constexpr unsigned kKernelIdAttnTc = 64;
+
+template <int D>
+struct TcSmem {
+  static constexpr uint32_t kQ = kTcRows * D * 2;  // D / 64 tiles of 128 rows x 128 bytes
+  static constexpr uint32_t kK = kKeys * D * 2;    // D / 64 tiles of 64 rows x 128 bytes
+  static constexpr uint32_t kV = D * kKeys * 2;    // D rows x 128 bytes
+  static constexpr uint32_t k = kQ;
+  static constexpr uint32_t v = k + 2 * kK;
+  static constexpr uint32_t bars = v + 2 * kV;
+  static constexpr uint32_t misc = bars + 16 * 8;
+  static constexpr size_t bytes = misc + 16 + 1024;
+};
+
+// TMEM columns: O, S, P (two fp16 per column).
+constexpr uint32_t kTmemO = 0, kTmemS = 128, kTmemP = 192, kTmemAll = 256;
+
+__device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok));
+  return ok != 0;
+}
+
+struct TcArgs {
+  Kv8Cache c;
+  Kv8Batch bt;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  int64_t ldq;
+  int q_heads, group, row_tiles;
+  float scale_log2;  // softmax scale * log2(e)
+};
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kTcThreads, 2)
+    kv8_attention_tc_kernel(const TcArgs a, unsigned* err) {
+  using SM = TcSmem<D>;
+  constexpr int kHalves = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw_addr);
+  const uint32_t bar = base + SM::bars;
+  const uint32_t q_full = bar, s_full = bar + 8, s_empty = bar + 16, p_full = bar + 24,
+                 pv_done = bar + 32, done_bar = bar + 40;
+  auto k_full = [&](int s) { return bar + 48u + 8u * s; };
+  auto k_empty = [&](int s) { return bar + 64u + 8u * s; };
+  auto v_full = [&](int s) { return bar + 80u + 8u * s; };
+  auto v_empty = [&](int s) { return bar + 96u + 8u * s; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + SM::misc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + SM::misc + 8);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Row tiles from the last to the first: later ones see more keys.
+  const int rt = a.row_tiles - 1 - static_cast<int>(blockIdx.x);
+  const int h = blockIdx.y % a.c.heads, b = blockIdx.y / a.c.heads;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 4);
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 4);
+    mbar_init(p_full, 4);
+    mbar_init(pv_done, 1);
+    mbar_init(done_bar, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(k_full(s), 4);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 4);
+      mbar_init(v_empty(s), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemAll);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Not before this CTA holds its TMEM: a dependent kernel that allocated
+  // first would wait for this one while it waits for its TMEM.
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const Kv8Seq s = kv8_sequence(a.bt, b, a.c.log_page);
+  if (s.bad && threadIdx.x == 0 && h == 0 && rt == 0) record_error(err, kErrBadIndex, kKernelIdAttnTc);
+  const int n_rows = s.n * a.group;
+  const int r0 = rt * kTcRows;
+  const int live_rows = n_rows - r0 < kTcRows ? n_rows - r0 : kTcRows;  // <= 0: nothing to do
+  const int keys = live_rows > 0 ? s.len - s.n + (r0 + live_rows - 1) / a.group + 1 : 0;
+  const int tiles = keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+  const int first_limit = s.len - s.n + r0 / a.group;
+  const int32_t* table = a.bt.table + static_cast<int64_t>(b) * a.bt.max_pages;
+  bool bad_page = false;
+  // The page of the 16 tokens from `tok` on, -1 if none holds them.
+  auto page_of = [&](int tok) {
+    if (tok >= keys) return -1;
+    const int p = __ldg(table + (tok >> a.c.log_page));
+    if (p < 0 || p >= a.c.num_pages) {
+      bad_page = true;
+      return -1;
+    }
+    return p;
+  };
+
+  if (warp < 4) {
+    // -------------------------------------------------------- softmax --
+    const int row = threadIdx.x;
+    const int r = r0 + row;
+    const bool live = row < live_rows;
+    const int tok = live ? r / a.group : 0;
+    const int limit = live ? s.len - s.n + tok : -1;
+    const int64_t out_row = static_cast<int64_t>(s.row0 + tok) * a.q_heads + h * a.group +
+                            (live ? r - tok * a.group : 0);
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    float back = 0.f;  // undoes the query scaling, times the softmax scale
+    if (tiles > 0) {
+      // This row of Q, scaled by a power of two, into the swizzled tiles; a
+      // negative softmax scale goes into the queries' signs.
+      const uint4* qr = reinterpret_cast<const uint4*>(
+          a.q + static_cast<int64_t>(s.row0 + tok) * a.ldq +
+          (h * a.group + (live ? r - tok * a.group : 0)) * D);
+      uint32_t big = 0;
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 u = live ? __ldg(qr + i) : make_uint4(0, 0, 0, 0);
+        big = __vmaxu2(big, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                                     __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
+      }
+      big = max(big & 0xFFFFu, big >> 16);
+      const int e = static_cast<int>(big >> 7) - 127;  // largest magnitude in [2^e, 2^(e+1))
+      const float mag = __int_as_float((min(7 - e, 126) + 127) << 23);
+      const float up = a.scale_log2 < 0.f ? -mag : mag;
+      back = __int_as_float((max(e - 7, -126) + 127) << 23) * fabsf(a.scale_log2);
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 u = live ? __ldg(qr + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const __half2 p = __floats2half2_rn(__uint_as_float(w[x] << 16) * up,
+                                              __uint_as_float(w[x] & 0xFFFF0000u) * up);
+          o[x] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        sts128(base + (i >> 3) * (kTcRows * 128) + sw128_offset(row, i & 7), o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    float m = -INFINITY;  // what O and l are relative to
+    float l = 0.f, v_ref = 0.f;
+    // Scales of the tile's four granules: lane g < 4 fetches those of granule
+    // g one tile ahead.
+    float sk_next = 0.f, sv_next = 0.f;
+    auto scales_of = [&](int j) {
+      const int p = (lane < 4 && j < tiles) ? page_of(j * kKeys + 16 * lane) : -1;
+      const int64_t at = static_cast<int64_t>(p < 0 ? 0 : p) * a.c.heads + h;
+      sk_next = p < 0 ? 0.f : __ldg(a.c.ks + at);
+      sv_next = p < 0 ? 0.f : __ldg(a.c.vs + at);
+    };
+    scales_of(0);
+    bool ok = true;
+    for (int j = 0; j < tiles; ++j) {
+      const int tok0 = j * kKeys;
+      float f[4], w[4];
+      float v_top = 0.f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f[g] = __shfl_sync(0xffffffffu, sk_next, g) * back;
+        w[g] = __shfl_sync(0xffffffffu, sv_next, g);
+        v_top = fmaxf(v_top, w[g]);
+      }
+      scales_of(j + 1);
+      const bool all_seen = tok0 + kKeys - 1 <= first_limit;  // by every row
+      const int seen = limit - tok0;  // columns 0 .. seen of the tile count
+
+      ok = mbar_wait(s_full, j & 1u, abort_flag, err, kKernelIdAttnTc);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sc[2][32];
+      tmem_ld32(lane_addr + kTmemS, sc[0]);
+      tmem_ld32(lane_addr + kTmemS + 32, sc[1]);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_empty);
+
+      // Largest score; masked scores (which may be anything) do not count.
+      float top = -INFINITY;
+      auto largest = [&](auto masks) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float t = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float v = __uint_as_float(sc[g >> 1][(g & 1) * 16 + x]);
+            if (!decltype(masks)::value || 16 * g + x <= seen) t = fmaxf(t, v);
+          }
+          top = fmaxf(top, t == -INFINITY ? t : t * f[g]);
+        }
+      };
+      if (all_seen) largest(std::false_type{}); else largest(std::true_type{});
+      // Move the reference maximum only where it has grown by 2^5 or there
+      // is none yet, and v_ref only where a value scale exceeds twice it.
+      const bool move_m = top > m + kTcGrow || (m == -INFINITY && top > -INFINITY);
+      const bool move_v = v_top > 2.f * v_ref;
+      float keep = 1.f;
+      if (move_m) {
+        keep = m == -INFINITY ? 0.f : ex2(m - top);
+        l *= keep;
+        m = top;
+      }
+      if (move_v) {
+        keep *= v_ref / v_top;
+        v_ref = v_top;
+      }
+      const float base_m = (m == -INFINITY ? 0.f : m) - kTcShift;
+      const float inv_v = v_ref > 0.f ? 1.f / v_ref : 0.f;
+      uint32_t p[32];
+      auto weights = [&](auto masks) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float wv = w[g] * inv_v;
+#pragma unroll
+          for (int x = 0; x < 16; x += 2) {
+            const float s0 = __uint_as_float(sc[g >> 1][(g & 1) * 16 + x]);
+            const float s1 = __uint_as_float(sc[g >> 1][(g & 1) * 16 + x + 1]);
+            float p0 = ex2(fmaf(s0, f[g], -base_m)), p1 = ex2(fmaf(s1, f[g], -base_m));
+            if (decltype(masks)::value) {
+              if (16 * g + x > seen) p0 = 0.f;
+              if (16 * g + x + 1 > seen) p1 = 0.f;
+            }
+            l += p0 + p1;
+            const __half2 q = __floats2half2_rn(p0 * wv, p1 * wv);
+            p[8 * g + x / 2] = *reinterpret_cast<const uint32_t*>(&q);
+          }
+        }
+      };
+      if (all_seen) weights(std::false_type{}); else weights(std::true_type{});
+      // The last tile's product has read P and written O.
+      if (j > 0) {
+        ok = mbar_wait(pv_done, (j - 1) & 1u, abort_flag, err, kKernelIdAttnTc);
+        if (!ok) break;
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, move_m || move_v)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(lane_addr + kTmemO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+            tmem_st32(lane_addr + kTmemO + c, o);
+          }
+        }
+      }
+      tmem_st32(lane_addr + kTmemP, p);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+    }
+    if (ok && tiles > 0) ok = mbar_wait(pv_done, (tiles - 1) & 1u, abort_flag, err, kKernelIdAttnTc);
+    tc_fence_after();
+    if (ok && live_rows > 0) {
+      // l is times 2^9 like P, so the factors cancel.
+      const float inv = l > 0.f ? v_ref / l : 0.f;
+      __nv_bfloat16* dst = a.out + out_row * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (tiles > 0) {
+          tmem_ld32(lane_addr + kTmemO + c, o);
+          tmem_ld_wait();
+        }
+        uint32_t y[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          // A row that sees nothing (l = 0) gets zeros whatever O holds.
+          const float y0 = inv > 0.f ? __uint_as_float(o[2 * x]) * inv : 0.f;
+          const float y1 = inv > 0.f ? __uint_as_float(o[2 * x + 1]) * inv : 0.f;
+          const __nv_bfloat162 q = __floats2bfloat162_rn(y0, y1);
+          y[x] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        if (live) {
+          uint4* d4 = reinterpret_cast<uint4*>(dst + c);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            d4[x] = make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
+        }
+      }
+    }
+  } else if (warp == 4) {
+    // ------------------------------------------------------------ MMA --
+    const bool one = elect_lane();
+    constexpr uint32_t idesc_s = idesc_f16(kTcRows, kKeys, false);
+    constexpr uint32_t idesc_o = idesc_f16(kTcRows, D, false);
+    bool issued = false;
+    auto scores = [&](int j) {
+      if (!mbar_wait(k_full(j & 1), (j >> 1) & 1u, abort_flag, err, kKernelIdAttnTc)) return false;
+      if (j > 0 && !mbar_wait(s_empty, (j - 1) & 1u, abort_flag, err, kKernelIdAttnTc)) return false;
+      tc_fence_after();
+      if (one) {
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+          const uint64_t da = sdesc_k_sw128(base + half * (kTcRows * 128));
+          const uint64_t db = sdesc_k_sw128(base + SM::k + (j & 1) * SM::kK + half * (kKeys * 128));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16(tmem + kTmemS, da + 2ull * kk, db + 2ull * kk, idesc_s, (half | kk) != 0);
+        }
+        umma_commit(s_full);
+        umma_commit(k_empty(j & 1));
+      }
+      issued = true;
+      return true;
+    };
+    bool ok = tiles > 0 && mbar_wait(q_full, 0, abort_flag, err, kKernelIdAttnTc);
+    ok = ok && scores(0);
+    for (int j = 0; ok && j < tiles; ++j) {
+      // The next scores before this tile's outputs: they run under its softmax.
+      if (j + 1 < tiles && !scores(j + 1)) break;
+      if (!mbar_wait(v_full(j & 1), (j >> 1) & 1u, abort_flag, err, kKernelIdAttnTc)) break;
+      if (!mbar_wait(p_full, j & 1u, abort_flag, err, kKernelIdAttnTc)) break;
+      tc_fence_after();
+      if (one) {
+        const uint64_t db = sdesc_k_sw128(base + SM::v + (j & 1) * SM::kV);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          umma_f16_ta(tmem + kTmemO, tmem + kTmemP + 8 * kk, db + 2ull * kk, idesc_o,
+                      (j | kk) != 0);
+        umma_commit(pv_done);
+        umma_commit(v_empty(j & 1));
+      }
+    }
+    if (*abort_flag && issued && one) {
+      umma_commit(done_bar);  // in-flight MMAs end before TMEM is freed
+      volatile int dummy = 0;
+      mbar_wait(done_bar, 0, &dummy, err, kKernelIdAttnTc, kWaitLimitNs / 4);
+    }
+  } else {
+    // ------------------------------------------------- dequantization --
+    const int t = threadIdx.x - 160;  // 0 .. 127
+    // Pieces of 16 codes.  Keys: token t % 8 + 8 (piece % 8), 16-channel
+    // chunk (t / 8 % 4) + 4 (...); values: channel and 16-token chunk alike:
+    // eight neighbouring lanes hold eight rows of one chunk, so their 16-byte
+    // stores meet different banks of the swizzled tile.
+    constexpr int kPieces = kKeys * D / 16 / 128;  // per thread and side: 4 or 2
+    uint4 kreg[kPieces], vreg[kPieces];
+    const int sub = t & 7, grp8 = t >> 3;  // 16 groups of 8 lanes
+    auto k_piece = [&](int i, int& row, int& chunk) {  // D / 16 chunks, 8 row groups
+      const int u = grp8 + 16 * i;
+      chunk = u % (D / 16);
+      row = (u / (D / 16)) * 8 + sub;
+    };
+    auto v_piece = [&](int i, int& row, int& chunk) {  // 4 chunks, D / 8 row groups
+      const int u = grp8 + 16 * i;
+      chunk = u & 3;
+      row = (u >> 2) * 8 + sub;
+    };
+    const int page_mask = (1 << a.c.log_page) - 1;
+    auto fetch_k = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        int row, chunk;
+        k_piece(i, row, chunk);
+        const int tok = j * kKeys + row;
+        const int p = j < tiles ? page_of(tok & ~15) : -1;
+        kreg[i] = make_uint4(0, 0, 0, 0);
+        if (p >= 0)
+          kreg[i] = __ldg(reinterpret_cast<const uint4*>(
+              a.c.k + (((static_cast<int64_t>(p) * a.c.heads + h) << a.c.log_page) +
+                       (tok & page_mask)) * D + 16 * chunk));
+      }
+    };
+    auto fetch_v = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        int row, chunk;
+        v_piece(i, row, chunk);
+        const int tok = j * kKeys + 16 * chunk;
+        const int p = j < tiles ? page_of(tok) : -1;
+        vreg[i] = make_uint4(0, 0, 0, 0);
+        if (p >= 0)
+          vreg[i] = __ldg(reinterpret_cast<const uint4*>(
+              a.c.v + (((static_cast<int64_t>(p) * a.c.heads + h) * D + row) << a.c.log_page) +
+              (tok & page_mask)));
+      }
+    };
+    auto put = [&](uint32_t tile, int row, int chunk, uint4 c) {
+      // 16 codes are two 16-byte chunks of the row's 128 bytes.
+      uint32_t o[8];
+      kv8_codes_to_f16<FMT>(c.x, o[0], o[1]);
+      kv8_codes_to_f16<FMT>(c.y, o[2], o[3]);
+      kv8_codes_to_f16<FMT>(c.z, o[4], o[5]);
+      kv8_codes_to_f16<FMT>(c.w, o[6], o[7]);
+      sts128(tile + sw128_offset(row, 2 * chunk), o[0], o[1], o[2], o[3]);
+      sts128(tile + sw128_offset(row, 2 * chunk + 1), o[4], o[5], o[6], o[7]);
+    };
+    fetch_k(0);
+    fetch_v(0);
+    for (int j = 0; j < tiles; ++j) {
+      const int st = j & 1;
+      if (j >= 2 && !mbar_wait(k_empty(st), ((j >> 1) - 1) & 1u, abort_flag, err, kKernelIdAttnTc))
+        break;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        int row, chunk;
+        k_piece(i, row, chunk);
+        put(base + SM::k + st * SM::kK + (chunk >> 2) * (kKeys * 128), row, chunk & 3, kreg[i]);
+      }
+      fetch_k(j + 1);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_full(st));
+      if (j >= 2 && !mbar_wait(v_empty(st), ((j >> 1) - 1) & 1u, abort_flag, err, kKernelIdAttnTc))
+        break;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        int row, chunk;
+        v_piece(i, row, chunk);
+        const int held = keys - (j * kKeys + 16 * chunk);  // tokens of these 16 that count
+        if (held < 16) {
+          // Bytes behind the last key may hold anything, NaN codes included.
+          uint32_t* c = reinterpret_cast<uint32_t*>(&vreg[i]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int nb = held - 4 * x;
+            c[x] &= nb >= 4 ? 0xFFFFFFFFu : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
+          }
+        }
+        put(base + SM::v + st * SM::kV, row, chunk, vreg[i]);
+      }
+      fetch_v(j + 1);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_full(st));
+    }
+  }
+  if (bad_page) record_error(err, kErrBadIndex, kKernelIdAttnTc);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemAll);
+  }
+}
+
+template <int FMT, int D>
+cudaError_t launch_tc(const TcArgs& a, cudaStream_t stream, unsigned* err) {
+  using SM = TcSmem<D>;
+  constexpr auto kern = kv8_attention_tc_kernel<FMT, D>;
+  static unsigned long long done = 0;  // bit d: device d
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(SM::bytes));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.row_tiles),
+                     static_cast<unsigned>(a.bt.batch) * a.c.heads, 1);
+  cfg.blockDim = dim3(kTcThreads, 1, 1);
+  cfg.dynamicSmemBytes = SM::bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, err);
+}
+
+}  // namespace
+
+bool kv8_attention_tc_fits(const Kv8Cache& c, const Kv8Batch& bt) {
+  return static_cast<int64_t>(bt.batch) * c.heads <= 65535;  // a grid axis
+}
+
+cudaError_t launch_kv8_attention_tc(const Kv8Cache& c, const Kv8Batch& bt, const void* q,
+                                    int64_t ldq, int q_heads, int D, int fmt, float scale,
+                                    void* out, cudaStream_t stream, unsigned* err) {
+  TcArgs a;
+  a.c = c;
+  a.bt = bt;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.ldq = ldq;
+  a.q_heads = q_heads;
+  a.group = q_heads / c.heads;
+  a.row_tiles = static_cast<int>((static_cast<int64_t>(bt.max_new) * a.group + kTcRows - 1) / kTcRows);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if (fmt == kKvInt8)
+    return D == 64 ? launch_tc<kKvInt8, 64>(a, stream, err) : launch_tc<kKvInt8, 128>(a, stream, err);
+  return D == 64 ? launch_tc<kKvE4m3, 64>(a, stream, err) : launch_tc<kKvE4m3, 128>(a, stream, err);
+}
+
+}  // namespace w4
