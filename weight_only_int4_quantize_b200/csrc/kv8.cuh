@@ -20,6 +20,27 @@ constexpr unsigned kErrBadIndex = 2u;
 
 __host__ __device__ constexpr float kv8_qmax(int fmt) { return fmt == kKvInt8 ? 127.f : 448.f; }
 
+// Asynchronous copies of 16 bytes (zeros unless live), waited for by the lane
+// that issued them.
+__device__ __forceinline__ void kv8_copy16(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void kv8_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void kv8_copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 kv8_lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
 // Four codes -> two packed pairs of fp16 values.
 template <int FMT>
 __device__ __forceinline__ void kv8_codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {

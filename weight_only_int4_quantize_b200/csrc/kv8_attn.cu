@@ -69,25 +69,6 @@ struct AttnSmem {
   static constexpr int bytes = ml + 2 * 16 * 4;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  const int n = live ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -193,7 +174,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         const uint8_t* src = a.c.v + head * D + in_page + (static_cast<int64_t>(g) << a.c.log_page);
 #pragma unroll
         for (int j = 0; j < 2 * kDTiles; ++j)
-          cp_async16(dst + j * 512, src + (static_cast<int64_t>(8 * j) << a.c.log_page), page >= 0);
+          kv8_copy16(dst + j * 512, src + (static_cast<int64_t>(8 * j) << a.c.log_page), page >= 0);
       } else {
         // tokens g % 2, g % 2 + 2, + 4, ... of granule g / 2
         const uint8_t* src = a.c.k + (head + in_page + (g & 1)) * D + 16 * t;
@@ -201,10 +182,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         for (int j = 0; j < 8; ++j)
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
-            cp_async16(dst + (j * kChunks + c) * 512, src + 2 * j * D + 64 * c, page >= 0);
+            kv8_copy16(dst + (j * kChunks + c) * 512, src + 2 * j * D + 64 * c, page >= 0);
       }
     }
-    cp_commit();
+    kv8_copy_commit();
   };
 #pragma unroll
   for (int u = 0; u < kSlots; ++u) issue(u);
@@ -281,7 +262,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     scales_of(i + 1, sk_next, sv_next);
     // ---- scores: sc[nt][i4][x], tokens 16 (g/2) + 4 i4 + g%2 (+ 2 for x >= 2)
     // of rows 2 t + x % 2 ----
-    cp_wait<kSlots - 1>();
+    kv8_copy_wait<kSlots - 1>();
     float sc[NT][4][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -296,7 +277,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         uint32_t kw[8][4];  // the lane's eight tokens
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint4 w = lds128(src + (j * kChunks + c) * 512);
+          const uint4 w = kv8_lds128(src + (j * kChunks + c) * 512);
           kw[j][0] = w.x, kw[j][1] = w.y, kw[j][2] = w.z, kw[j][3] = w.w;
         }
 #pragma unroll
@@ -363,7 +344,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         for (int x = 0; x < 4; ++x) o[nt][j][x] *= keep[x & 1];
     }
     // ---- outputs ----
-    cp_wait<kSlots - 1>();
+    kv8_copy_wait<kSlots - 1>();
     {
       const uint32_t src = ring + ((2 * i + 1) % kSlots) * SM::kSlotBytes;
       // Bytes behind the last key may hold anything, NaN codes included.
@@ -374,7 +355,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         uint32_t vw[8][4];  // four output tiles: channels g and g + 8 of each
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint4 w = lds128(src + (2 * j0 + j) * 512);
+          const uint4 w = kv8_lds128(src + (2 * j0 + j) * 512);
           vw[j][0] = w.x, vw[j][1] = w.y, vw[j][2] = w.z, vw[j][3] = w.w;
         }
 #pragma unroll
@@ -398,7 +379,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     }
     issue(2 * i + 1 + kSlots);
   }
-  cp_wait<0>();
+  kv8_copy_wait<0>();
   if (bad_page) record_error(err, kErrBadIndex, kKernelIdAttn);
 
   // ---- join the warps of the CTA ----

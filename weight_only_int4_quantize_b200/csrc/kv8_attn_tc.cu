@@ -1,19 +1,29 @@
 // Causal attention over the 8-bit paged cache (layout: kv8.cuh), tcgen05
 // kernel: long runs of new tokens (prompts and their chunks).
 //
-// One CTA owns 128 rows (row = token * group + head of the group) of one
-// sequence and kv head and walks the keys in tiles of 64:
+// One CTA owns 256 rows (row = token * group + head of the group), two tiles
+// of 128, of one sequence and kv head and walks the keys in tiles of 64:
 //
 //   S = Q K^T            (fp16 operands, fp32 in TMEM)
 //   P = exp2(f S - m)    (fp16 in TMEM, weighted by the value scales)
 //   O += P V             (A operand P from TMEM, fp32 accumulator in TMEM)
 //
-// Warp roles: 0..3 softmax (a thread owns a row), 4 MMA issue, 5..8
-// dequantization: they fetch the codes of the next tile into registers, turn
-// those of this one into fp16 and write the swizzled operand tiles, so codes
-// cross L2 once per 128 rows and never shared memory as bytes.  Two CTAs share
-// an SM, so one's exponentials run under the other's products: per tile the
-// tensor pipe and the exponential unit need 512 cycles each.
+// Warp roles: 0..3 and 4..7 softmax of the two row tiles (a thread owns a
+// row), 8 and 9 MMA issue for one row tile each, 10..13 dequantization: a
+// lane copies (cp.async) the pieces of codes that it will turn three tiles
+// ahead, turns this tile's into fp16 and writes the swizzled operand tiles, so
+// codes cross L2 once per 256 rows.
+//
+// Per row tile and 64 keys (D = 128) the tensor pipe needs 512 cycles (640
+// with the shared-memory reads of the score product) and the exponential unit
+// 512; what has to be kept out of the way is latency.  S is released once it
+// is in registers, so the next scores run under the exponentials; P has two
+// buffers, so a row tile's softmax never waits for its outputs; each row tile
+// has its own issuing warp, so one does not wait for the other's softmax.
+// 2 x 2048 tokens over up to 8192 keys, 16 / 8 heads: 128 rows per CTA and
+// two CTAs per SM 371 us; 256 rows, one issuing warp, codes fetched into
+// registers one tile ahead 340 us (with the fetches taken out 238 us, with
+// all but the handshakes taken out 163 us).
 //
 // Numerics as in the rows kernel (kv8_attn.cu): codes are exact in fp16; a
 // query row is scaled by a power of two; key scales (one per 16 keys at the
@@ -33,8 +43,10 @@ namespace w4 {
 
 namespace {
 
-constexpr int kTcThreads = 288;
-constexpr int kTcRows = 128;
+constexpr int kTcThreads = 448;
+constexpr int kTcRows = 128;         // rows of one MMA; two such tiles per CTA
+constexpr int kTcStages = 3;         // key and value tiles in shared memory
+constexpr int kTcAhead = 3;          // tiles of codes on their way
 constexpr int kKeys = 64;            // keys of a tile
 constexpr float kTcShift = 9.f;      // probabilities are kept times 2^9
 constexpr float kTcGrow = 5.f;       // the maximum moves once a row's has grown by 2^5
@@ -45,15 +57,17 @@ struct TcSmem {
   static constexpr uint32_t kQ = kTcRows * D * 2;  // D / 64 tiles of 128 rows x 128 bytes
   static constexpr uint32_t kK = kKeys * D * 2;    // D / 64 tiles of 64 rows x 128 bytes
   static constexpr uint32_t kV = D * kKeys * 2;    // D rows x 128 bytes
-  static constexpr uint32_t k = kQ;
-  static constexpr uint32_t v = k + 2 * kK;
-  static constexpr uint32_t bars = v + 2 * kV;
-  static constexpr uint32_t misc = bars + 16 * 8;
-  static constexpr size_t bytes = misc + 16 + 1024;
+  static constexpr uint32_t k = 2 * kQ;
+  static constexpr uint32_t v = k + kTcStages * kK;
+  static constexpr uint32_t codes = v + kTcStages * kV;  // keys, values in turn
+  static constexpr uint32_t kCodes = kKeys * D;
+  static constexpr uint32_t bars = codes + 2 * kTcAhead * kCodes;
+  static constexpr uint32_t misc = bars + (14 + 4 * kTcStages) * 8;
+  static constexpr size_t bytes = misc + 32 + 1024;
 };
 
-// TMEM columns: O, S, P (two fp16 per column).
-constexpr uint32_t kTmemO = 0, kTmemS = 128, kTmemP = 192, kTmemAll = 256;
+// TMEM columns: O and S of both row tiles, two P each (two fp16 per column).
+constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemP = 384, kTmemAll = 512;
 
 __device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -97,6 +111,30 @@ __device__ __forceinline__ float ex2(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
@@ -119,7 +157,7 @@ struct TcArgs {
 };
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kTcThreads, 2)
+__global__ void __launch_bounds__(kTcThreads, 1)
     kv8_attention_tc_kernel(const TcArgs a, unsigned* err) {
   using SM = TcSmem<D>;
   constexpr int kHalves = D / 64;
@@ -128,12 +166,20 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - raw_addr);
   const uint32_t bar = base + SM::bars;
-  const uint32_t q_full = bar, s_full = bar + 8, s_empty = bar + 16, p_full = bar + 24,
-                 pv_done = bar + 32, done_bar = bar + 40;
-  auto k_full = [&](int s) { return bar + 48u + 8u * s; };
-  auto k_empty = [&](int s) { return bar + 64u + 8u * s; };
-  auto v_full = [&](int s) { return bar + 80u + 8u * s; };
-  auto v_empty = [&](int s) { return bar + 96u + 8u * s; };
+  // One of each per row tile.
+  auto q_full = [&](int t) { return bar + 8u * t; };
+  auto s_full = [&](int t) { return bar + 16u + 8u * t; };
+  auto s_empty = [&](int t) { return bar + 32u + 8u * t; };
+  // P has a barrier per buffer: a warp may be a key tile ahead of another (it
+  // needs only that all have read S), and its arrival must not count for the
+  // slower one's tile.
+  auto p_full = [&](int t, int buf) { return bar + 48u + 8u * (2 * t + buf); };
+  auto pv_done = [&](int t) { return bar + 80u + 8u * t; };
+  auto done_bar = [&](int t) { return bar + 96u + 8u * t; };
+  auto k_full = [&](int s) { return bar + 112u + 8u * s; };
+  auto k_empty = [&](int s) { return bar + 112u + 8u * (kTcStages + s); };
+  auto v_full = [&](int s) { return bar + 112u + 8u * (2 * kTcStages + s); };
+  auto v_empty = [&](int s) { return bar + 112u + 8u * (3 * kTcStages + s); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + SM::misc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + SM::misc + 8);
 
@@ -143,22 +189,25 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   const int h = blockIdx.y % a.c.heads, b = blockIdx.y / a.c.heads;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 4);
-    mbar_init(s_full, 1);
-    mbar_init(s_empty, 4);
-    mbar_init(p_full, 4);
-    mbar_init(pv_done, 1);
-    mbar_init(done_bar, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), 4);
+      mbar_init(s_full(t), 1);
+      mbar_init(s_empty(t), 4);
+      mbar_init(p_full(t, 0), 4);
+      mbar_init(p_full(t, 1), 4);
+      mbar_init(pv_done(t), 1);
+      mbar_init(done_bar(t), 1);
+    }
+    for (int s = 0; s < kTcStages; ++s) {
       mbar_init(k_full(s), 4);
-      mbar_init(k_empty(s), 1);
+      mbar_init(k_empty(s), 2);  // both issuing warps
       mbar_init(v_full(s), 4);
-      mbar_init(v_empty(s), 1);
+      mbar_init(v_empty(s), 2);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(smem_u32(tmem_slot), kTmemAll);
     tmem_relinquish();
   }
@@ -174,11 +223,22 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   const Kv8Seq s = kv8_sequence(a.bt, b, a.c.log_page);
   if (s.bad && threadIdx.x == 0 && h == 0 && rt == 0) record_error(err, kErrBadIndex, kKernelIdAttnTc);
   const int n_rows = s.n * a.group;
-  const int r0 = rt * kTcRows;
-  const int live_rows = n_rows - r0 < kTcRows ? n_rows - r0 : kTcRows;  // <= 0: nothing to do
-  const int keys = live_rows > 0 ? s.len - s.n + (r0 + live_rows - 1) / a.group + 1 : 0;
-  const int tiles = keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
-  const int first_limit = s.len - s.n + r0 / a.group;
+  // Rows, keys seen (by the last row) and key tiles of each row tile; the
+  // second's rows are later tokens, so it has at least as many key tiles
+  // unless it has no rows.
+  auto rows_of = [&](int t) {
+    const int left = n_rows - (2 * rt + t) * kTcRows;
+    return left < 0 ? 0 : left < kTcRows ? left : kTcRows;
+  };
+  auto keys_of = [&](int t) {
+    const int n = rows_of(t);
+    const int k = n > 0 ? s.len - s.n + ((2 * rt + t) * kTcRows + n - 1) / a.group + 1 : 0;
+    return k > 0 ? k : 0;
+  };
+  const int keys0 = keys_of(0), keys1 = keys_of(1);
+  const int keys = keys0 > keys1 ? keys0 : keys1;
+  const int tiles0 = (keys0 + kKeys - 1) / kKeys, tiles1 = (keys1 + kKeys - 1) / kKeys;
+  const int tiles = (keys + kKeys - 1) / kKeys;
   const int32_t* table = a.bt.table + static_cast<int64_t>(b) * a.bt.max_pages;
   bool bad_page = false;
   // The page of the 16 tokens from `tok` on, -1 if none holds them.
@@ -192,18 +252,24 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     return p;
   };
 
-  if (warp < 4) {
+  if (warp < 8) {
     // -------------------------------------------------------- softmax --
-    const int row = threadIdx.x;
+    const int rtile = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const int r0 = (2 * rt + rtile) * kTcRows;
     const int r = r0 + row;
-    const bool live = row < live_rows;
+    const bool live = row < rows_of(rtile);
+    const int my_tiles = rtile ? tiles1 : tiles0;
+    const int first_limit = s.len - s.n + r0 / a.group;  // what every row sees
     const int tok = live ? r / a.group : 0;
     const int limit = live ? s.len - s.n + tok : -1;
     const int64_t out_row = static_cast<int64_t>(s.row0 + tok) * a.q_heads + h * a.group +
                             (live ? r - tok * a.group : 0);
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t t_o = lane_addr + kTmemO + 128 * rtile, t_s = lane_addr + kTmemS + 64 * rtile,
+                   t_p = lane_addr + kTmemP + 64 * rtile;
     float back = 0.f;  // undoes the query scaling, times the softmax scale
-    if (tiles > 0) {
+    if (my_tiles > 0) {
       // This row of Q, scaled by a power of two, into the swizzled tiles; a
       // negative softmax scale goes into the queries' signs.
       const uint4* qr = reinterpret_cast<const uint4*>(
@@ -230,26 +296,28 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                               __uint_as_float(w[x] & 0xFFFF0000u) * up);
           o[x] = *reinterpret_cast<const uint32_t*>(&p);
         }
-        sts128(base + (i >> 3) * (kTcRows * 128) + sw128_offset(row, i & 7), o[0], o[1], o[2], o[3]);
+        sts128(base + rtile * SM::kQ + (i >> 3) * (kTcRows * 128) + sw128_offset(row, i & 7), o[0],
+               o[1], o[2], o[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) mbar_arrive(q_full(rtile));
     }
     float m = -INFINITY;  // what O and l are relative to
-    float l = 0.f, v_ref = 0.f;
+    float v_ref = 0.f;
+    uint64_t l2 = pack2(0.f, 0.f);  // the sum, in two halves
     // Scales of the tile's four granules: lane g < 4 fetches those of granule
     // g one tile ahead.
     float sk_next = 0.f, sv_next = 0.f;
     auto scales_of = [&](int j) {
-      const int p = (lane < 4 && j < tiles) ? page_of(j * kKeys + 16 * lane) : -1;
+      const int p = (lane < 4 && j < my_tiles) ? page_of(j * kKeys + 16 * lane) : -1;
       const int64_t at = static_cast<int64_t>(p < 0 ? 0 : p) * a.c.heads + h;
       sk_next = p < 0 ? 0.f : __ldg(a.c.ks + at);
       sv_next = p < 0 ? 0.f : __ldg(a.c.vs + at);
     };
     scales_of(0);
     bool ok = true;
-    for (int j = 0; j < tiles; ++j) {
+    for (int j = 0; j < my_tiles; ++j) {
       const int tok0 = j * kKeys;
       float f[4], w[4];
       float v_top = 0.f;
@@ -260,19 +328,19 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         v_top = fmaxf(v_top, w[g]);
       }
       scales_of(j + 1);
-      const bool all_seen = tok0 + kKeys - 1 <= first_limit;  // by every row
+      const bool all_seen = tok0 + kKeys - 1 <= first_limit;  // by every live row
       const int seen = limit - tok0;  // columns 0 .. seen of the tile count
 
-      ok = mbar_wait(s_full, j & 1u, abort_flag, err, kKernelIdAttnTc);
+      ok = mbar_wait(s_full(rtile), j & 1u, abort_flag, err, kKernelIdAttnTc);
       if (!ok) break;
       tc_fence_after();
       uint32_t sc[2][32];
-      tmem_ld32(lane_addr + kTmemS, sc[0]);
-      tmem_ld32(lane_addr + kTmemS + 32, sc[1]);
+      tmem_ld32(t_s, sc[0]);
+      tmem_ld32(t_s + 32, sc[1]);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(s_empty);
+      if (lane == 0) mbar_arrive(s_empty(rtile));
 
       // Largest score; masked scores (which may be anything) do not count.
       float top = -INFINITY;
@@ -296,70 +364,85 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       float keep = 1.f;
       if (move_m) {
         keep = m == -INFINITY ? 0.f : ex2(m - top);
-        l *= keep;
+        l2 = mul2(l2, pack2(keep, keep));
         m = top;
       }
       if (move_v) {
         keep *= v_ref / v_top;
         v_ref = v_top;
       }
-      const float base_m = (m == -INFINITY ? 0.f : m) - kTcShift;
-      const float inv_v = v_ref > 0.f ? 1.f / v_ref : 0.f;
+      const float off = kTcShift - (m == -INFINITY ? 0.f : m);
+      const uint64_t off2 = pack2(off, off);
+      const float inv_v = v_ref > 0.f ? __frcp_rn(v_ref) : 0.f;
       uint32_t p[32];
       auto weights = [&](auto masks) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const float wv = w[g] * inv_v;
+          const uint64_t f2 = pack2(f[g], f[g]), w2 = pack2(wv, wv);
 #pragma unroll
           for (int x = 0; x < 16; x += 2) {
-            const float s0 = __uint_as_float(sc[g >> 1][(g & 1) * 16 + x]);
-            const float s1 = __uint_as_float(sc[g >> 1][(g & 1) * 16 + x + 1]);
-            float p0 = ex2(fmaf(s0, f[g], -base_m)), p1 = ex2(fmaf(s1, f[g], -base_m));
+            const uint64_t e2 =
+                fma2(pack2(__uint_as_float(sc[g >> 1][(g & 1) * 16 + x]),
+                           __uint_as_float(sc[g >> 1][(g & 1) * 16 + x + 1])), f2, off2);
+            float p0, p1;
+            unpack2(e2, p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
             if (decltype(masks)::value) {
               if (16 * g + x > seen) p0 = 0.f;
               if (16 * g + x + 1 > seen) p1 = 0.f;
             }
-            l += p0 + p1;
-            const __half2 q = __floats2half2_rn(p0 * wv, p1 * wv);
+            const uint64_t p2 = pack2(p0, p1);
+            l2 = add2(l2, p2);
+            unpack2(mul2(p2, w2), p0, p1);
+            const __half2 q = __floats2half2_rn(p0, p1);
             p[8 * g + x / 2] = *reinterpret_cast<const uint32_t*>(&q);
           }
         }
       };
       if (all_seen) weights(std::false_type{}); else weights(std::true_type{});
-      // The last tile's product has read P and written O.
-      if (j > 0) {
-        ok = mbar_wait(pv_done, (j - 1) & 1u, abort_flag, err, kKernelIdAttnTc);
+      // O is moved between products: all up to the last tile's are done and
+      // this tile's waits for P.
+      if (j > 0 && __any_sync(0xffffffffu, move_m || move_v)) {
+        ok = mbar_wait(pv_done(rtile), (j - 1) & 1u, abort_flag, err, kKernelIdAttnTc);
         if (!ok) break;
         tc_fence_after();
-        if (__any_sync(0xffffffffu, move_m || move_v)) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(lane_addr + kTmemO + c, o);
-            tmem_ld_wait();
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(t_o + c, o);
+          tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
-            tmem_st32(lane_addr + kTmemO + c, o);
-          }
+          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+          tmem_st32(t_o + c, o);
         }
       }
-      tmem_st32(lane_addr + kTmemP, p);
+      // This P buffer was read by the product before the last, which ended
+      // before the last one's scores were committed (s_full below).
+      tmem_st32(t_p + 32 * (j & 1), p);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) mbar_arrive(p_full(rtile, j & 1));
     }
-    if (ok && tiles > 0) ok = mbar_wait(pv_done, (tiles - 1) & 1u, abort_flag, err, kKernelIdAttnTc);
+    // The last two products (the one before them ended before the last scores
+    // were committed), each phase in turn.
+    for (int j = my_tiles > 1 ? my_tiles - 2 : 0; ok && j < my_tiles; ++j)
+      ok = mbar_wait(pv_done(rtile), j & 1u, abort_flag, err, kKernelIdAttnTc);
     tc_fence_after();
-    if (ok && live_rows > 0) {
+    if (ok && rows_of(rtile) > 0) {
       // l is times 2^9 like P, so the factors cancel.
+      float la, lb;
+      unpack2(l2, la, lb);
+      const float l = la + lb;
       const float inv = l > 0.f ? v_ref / l : 0.f;
       __nv_bfloat16* dst = a.out + out_row * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
-        if (tiles > 0) {
-          tmem_ld32(lane_addr + kTmemO + c, o);
+        if (my_tiles > 0) {
+          tmem_ld32(t_o + c, o);
           tmem_ld_wait();
         }
         uint32_t y[16];
@@ -379,102 +462,121 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
       }
     }
-  } else if (warp == 4) {
+  } else if (warp < 10) {
     // ------------------------------------------------------------ MMA --
     const bool one = elect_lane();
+    const int t = warp - 8;
     constexpr uint32_t idesc_s = idesc_f16(kTcRows, kKeys, false);
     constexpr uint32_t idesc_o = idesc_f16(kTcRows, D, false);
+    const int my_tiles = t ? tiles1 : tiles0;
+    const uint32_t t_s = tmem + kTmemS + 64 * t, t_o = tmem + kTmemO + 128 * t,
+                   t_p = tmem + kTmemP + 64 * t;
     bool issued = false;
-    auto scores = [&](int j) {
-      if (!mbar_wait(k_full(j & 1), (j >> 1) & 1u, abort_flag, err, kKernelIdAttnTc)) return false;
-      if (j > 0 && !mbar_wait(s_empty, (j - 1) & 1u, abort_flag, err, kKernelIdAttnTc)) return false;
+    // Scores of key tile j (stage st, its phase ph).
+    auto scores = [&](int j, int st, uint32_t ph) {
+      if (!mbar_wait(k_full(st), ph, abort_flag, err, kKernelIdAttnTc)) return false;
+      if (j > 0 && !mbar_wait(s_empty(t), (j - 1) & 1u, abort_flag, err, kKernelIdAttnTc))
+        return false;
       tc_fence_after();
       if (one) {
 #pragma unroll
         for (int half = 0; half < kHalves; ++half) {
-          const uint64_t da = sdesc_k_sw128(base + half * (kTcRows * 128));
-          const uint64_t db = sdesc_k_sw128(base + SM::k + (j & 1) * SM::kK + half * (kKeys * 128));
+          const uint64_t da = sdesc_k_sw128(base + t * SM::kQ + half * (kTcRows * 128));
+          const uint64_t db = sdesc_k_sw128(base + SM::k + st * SM::kK + half * (kKeys * 128));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_f16(tmem + kTmemS, da + 2ull * kk, db + 2ull * kk, idesc_s, (half | kk) != 0);
+            umma_f16(t_s, da + 2ull * kk, db + 2ull * kk, idesc_s, (half | kk) != 0);
         }
-        umma_commit(s_full);
-        umma_commit(k_empty(j & 1));
+        umma_commit(s_full(t));
+        umma_commit(k_empty(st));
       }
       issued = true;
       return true;
     };
-    bool ok = tiles > 0 && mbar_wait(q_full, 0, abort_flag, err, kKernelIdAttnTc);
-    ok = ok && scores(0);
-    for (int j = 0; ok && j < tiles; ++j) {
+    bool ok = true;
+    if (my_tiles > 0)
+      ok = mbar_wait(q_full(t), 0, abort_flag, err, kKernelIdAttnTc) && scores(0, 0, 0);
+    int st = 0, nst = 1;
+    uint32_t ph = 0, nph = 0;
+    for (int j = 0; ok && j < my_tiles; ++j) {
       // The next scores before this tile's outputs: they run under its softmax.
-      if (j + 1 < tiles && !scores(j + 1)) break;
-      if (!mbar_wait(v_full(j & 1), (j >> 1) & 1u, abort_flag, err, kKernelIdAttnTc)) break;
-      if (!mbar_wait(p_full, j & 1u, abort_flag, err, kKernelIdAttnTc)) break;
+      if (j + 1 < my_tiles && !scores(j + 1, nst, nph)) break;
+      if (!mbar_wait(v_full(st), ph, abort_flag, err, kKernelIdAttnTc)) break;
+      if (!mbar_wait(p_full(t, j & 1), (j >> 1) & 1u, abort_flag, err, kKernelIdAttnTc)) break;
       tc_fence_after();
       if (one) {
-        const uint64_t db = sdesc_k_sw128(base + SM::v + (j & 1) * SM::kV);
+        const uint64_t db = sdesc_k_sw128(base + SM::v + st * SM::kV);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_f16_ta(tmem + kTmemO, tmem + kTmemP + 8 * kk, db + 2ull * kk, idesc_o,
-                      (j | kk) != 0);
-        umma_commit(pv_done);
-        umma_commit(v_empty(j & 1));
+          umma_f16_ta(t_o, t_p + 32 * (j & 1) + 8 * kk, db + 2ull * kk, idesc_o, (j | kk) != 0);
+        umma_commit(pv_done(t));
+        umma_commit(v_empty(st));
       }
+      st = nst;
+      ph = nph;
+      if (++nst == kTcStages) nst = 0, nph ^= 1u;
+    }
+    // Key tiles that only the other row tile has: release them as they come.
+    for (int j = my_tiles; ok && j < tiles && !*abort_flag; ++j) {
+      const int s3 = j % kTcStages;
+      const uint32_t p3 = (j / kTcStages) & 1u;
+      if (!mbar_wait(k_full(s3), p3, abort_flag, err, kKernelIdAttnTc)) break;
+      if (one) mbar_arrive(k_empty(s3));
+      if (!mbar_wait(v_full(s3), p3, abort_flag, err, kKernelIdAttnTc)) break;
+      if (one) mbar_arrive(v_empty(s3));
     }
     if (*abort_flag && issued && one) {
-      umma_commit(done_bar);  // in-flight MMAs end before TMEM is freed
+      umma_commit(done_bar(t));  // in-flight MMAs end before TMEM is freed
       volatile int dummy = 0;
-      mbar_wait(done_bar, 0, &dummy, err, kKernelIdAttnTc, kWaitLimitNs / 4);
+      mbar_wait(done_bar(t), 0, &dummy, err, kKernelIdAttnTc, kWaitLimitNs / 4);
     }
   } else {
     // ------------------------------------------------- dequantization --
-    const int t = threadIdx.x - 160;  // 0 .. 127
-    // Pieces of 16 codes.  Keys: token t % 8 + 8 (piece % 8), 16-channel
-    // chunk (t / 8 % 4) + 4 (...); values: channel and 16-token chunk alike:
-    // eight neighbouring lanes hold eight rows of one chunk, so their 16-byte
-    // stores meet different banks of the swizzled tile.
+    const int t = threadIdx.x - 320;  // 0 .. 127
+    // Pieces of 16 codes: eight neighbouring lanes hold eight rows (tokens of
+    // keys, channels of values) of one 16-code chunk, so their 16-byte stores
+    // meet different banks of the swizzled tile.
     constexpr int kPieces = kKeys * D / 16 / 128;  // per thread and side: 4 or 2
-    uint4 kreg[kPieces], vreg[kPieces];
+    constexpr int kChunks = D / 16;                // chunks of a key row
     const int sub = t & 7, grp8 = t >> 3;  // 16 groups of 8 lanes
-    auto k_piece = [&](int i, int& row, int& chunk) {  // D / 16 chunks, 8 row groups
-      const int u = grp8 + 16 * i;
-      chunk = u % (D / 16);
-      row = (u / (D / 16)) * 8 + sub;
-    };
-    auto v_piece = [&](int i, int& row, int& chunk) {  // 4 chunks, D / 8 row groups
-      const int u = grp8 + 16 * i;
-      chunk = u & 3;
-      row = (u >> 2) * 8 + sub;
-    };
+    // Keys: piece i is token k_row(i), chunk k_chunk; values: channel v_row(i),
+    // tokens 16 v_chunk ..
+    const int k_chunk = grp8 % kChunks;
+    auto k_row = [&](int i) { return (grp8 / kChunks + i * (16 / kChunks)) * 8 + sub; };
+    const int v_chunk = grp8 & 3;
+    auto v_row = [&](int i) { return ((grp8 >> 2) + 4 * i) * 8 + sub; };
     const int page_mask = (1 << a.c.log_page) - 1;
-    auto fetch_k = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        int row, chunk;
-        k_piece(i, row, chunk);
-        const int tok = j * kKeys + row;
-        const int p = j < tiles ? page_of(tok & ~15) : -1;
-        kreg[i] = make_uint4(0, 0, 0, 0);
-        if (p >= 0)
-          kreg[i] = __ldg(reinterpret_cast<const uint4*>(
-              a.c.k + (((static_cast<int64_t>(p) * a.c.heads + h) << a.c.log_page) +
-                       (tok & page_mask)) * D + 16 * chunk));
-      }
+    // Bytes from page to page (keys and values alike), and of this head.
+    const int64_t page_bytes = (static_cast<int64_t>(a.c.heads) << a.c.log_page) * D;
+    const int64_t head_bytes = (static_cast<int64_t>(h) << a.c.log_page) * D;
+    // Page ids of a tile's four granules, in the lanes g < 4.
+    auto pages = [&](int j) {
+      return (lane < 4 && j < tiles) ? page_of(j * kKeys + 16 * lane) : -1;
     };
-    auto fetch_v = [&](int j) {
+    // Each lane's own ring: keys and values of kTcAhead tiles, read back only
+    // by the lane that copied them.
+    const uint32_t own = base + SM::codes + 16u * t;
+    auto copy_k = [&](int j, int slot, int id) {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        int row, chunk;
-        v_piece(i, row, chunk);
-        const int tok = j * kKeys + 16 * chunk;
-        const int p = j < tiles ? page_of(tok) : -1;
-        vreg[i] = make_uint4(0, 0, 0, 0);
-        if (p >= 0)
-          vreg[i] = __ldg(reinterpret_cast<const uint4*>(
-              a.c.v + (((static_cast<int64_t>(p) * a.c.heads + h) * D + row) << a.c.log_page) +
-              (tok & page_mask)));
+        const int row = k_row(i);
+        const int p = __shfl_sync(0xffffffffu, id, row >> 4);
+        kv8_copy16(own + slot * 2 * SM::kCodes + i * 2048u,
+                   a.c.k + (p < 0 ? 0 : p) * page_bytes + head_bytes +
+                       ((j * kKeys + row) & page_mask) * D + 16 * k_chunk,
+                   p >= 0);
       }
+      kv8_copy_commit();
+    };
+    auto copy_v = [&](int j, int slot, int id) {
+      const int p = __shfl_sync(0xffffffffu, id, v_chunk);
+      const uint8_t* src = a.c.v + (p < 0 ? 0 : p) * page_bytes + head_bytes +
+                           ((j * kKeys + 16 * v_chunk) & page_mask);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        kv8_copy16(own + (slot * 2 + 1) * SM::kCodes + i * 2048u,
+                   src + (v_row(i) << a.c.log_page), p >= 0);
+      kv8_copy_commit();
     };
     auto put = [&](uint32_t tile, int row, int chunk, uint4 c) {
       // 16 codes are two 16-byte chunks of the row's 128 bytes.
@@ -483,54 +585,61 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       kv8_codes_to_f16<FMT>(c.y, o[2], o[3]);
       kv8_codes_to_f16<FMT>(c.z, o[4], o[5]);
       kv8_codes_to_f16<FMT>(c.w, o[6], o[7]);
-      sts128(tile + sw128_offset(row, 2 * chunk), o[0], o[1], o[2], o[3]);
-      sts128(tile + sw128_offset(row, 2 * chunk + 1), o[4], o[5], o[6], o[7]);
+      const uint32_t at = tile + sw128_offset(row, 2 * chunk);
+      sts128(at, o[0], o[1], o[2], o[3]);
+      sts128(at ^ 16u, o[4], o[5], o[6], o[7]);  // the neighbouring chunk
     };
-    fetch_k(0);
-    fetch_v(0);
+    for (int j = 0; j < kTcAhead; ++j) {
+      const int id = pages(j);
+      copy_k(j, j, id);
+      copy_v(j, j, id);
+    }
+    int id_next = pages(kTcAhead);
+    int st = 0, slot = 0;
+    uint32_t ph = 1;  // phase of the stage's release to wait for
     for (int j = 0; j < tiles; ++j) {
-      const int st = j & 1;
-      if (j >= 2 && !mbar_wait(k_empty(st), ((j >> 1) - 1) & 1u, abort_flag, err, kKernelIdAttnTc))
-        break;
+      const int id = id_next;  // of tile j + kTcAhead
+      id_next = pages(j + kTcAhead + 1);
+      if (j >= kTcStages && !mbar_wait(k_empty(st), ph, abort_flag, err, kKernelIdAttnTc)) break;
+      kv8_copy_wait<2 * kTcAhead - 1>();
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        int row, chunk;
-        k_piece(i, row, chunk);
-        put(base + SM::k + st * SM::kK + (chunk >> 2) * (kKeys * 128), row, chunk & 3, kreg[i]);
-      }
-      fetch_k(j + 1);
+      for (int i = 0; i < kPieces; ++i)
+        put(base + SM::k + st * SM::kK + (k_chunk >> 2) * (kKeys * 128), k_row(i), k_chunk & 3,
+            kv8_lds128(own + slot * 2 * SM::kCodes + i * 2048u));
+      copy_k(j + kTcAhead, slot, id);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full(st));
-      if (j >= 2 && !mbar_wait(v_empty(st), ((j >> 1) - 1) & 1u, abort_flag, err, kKernelIdAttnTc))
-        break;
+      if (j >= kTcStages && !mbar_wait(v_empty(st), ph, abort_flag, err, kKernelIdAttnTc)) break;
+      kv8_copy_wait<2 * kTcAhead - 1>();
+      const int held = keys - (j * kKeys + 16 * v_chunk);  // tokens of these 16 that count
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        int row, chunk;
-        v_piece(i, row, chunk);
-        const int held = keys - (j * kKeys + 16 * chunk);  // tokens of these 16 that count
+        uint4 c = kv8_lds128(own + (slot * 2 + 1) * SM::kCodes + i * 2048u);
         if (held < 16) {
           // Bytes behind the last key may hold anything, NaN codes included.
-          uint32_t* c = reinterpret_cast<uint32_t*>(&vreg[i]);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          auto mask = [&](uint32_t v, int x) {
             const int nb = held - 4 * x;
-            c[x] &= nb >= 4 ? 0xFFFFFFFFu : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
-          }
+            return nb >= 4 ? v : nb <= 0 ? 0u : v & ((1u << (8 * nb)) - 1u);
+          };
+          c = make_uint4(mask(c.x, 0), mask(c.y, 1), mask(c.z, 2), mask(c.w, 3));
         }
-        put(base + SM::v + st * SM::kV, row, chunk, vreg[i]);
+        put(base + SM::v + st * SM::kV, v_row(i), v_chunk, c);
       }
-      fetch_v(j + 1);
+      copy_v(j + kTcAhead, slot, id);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full(st));
+      if (++st == kTcStages) st = 0, ph ^= 1u;
+      if (++slot == kTcAhead) slot = 0;
     }
+    kv8_copy_wait<0>();
   }
   if (bad_page) record_error(err, kErrBadIndex, kKernelIdAttnTc);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 8) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemAll);
@@ -582,7 +691,8 @@ cudaError_t launch_kv8_attention_tc(const Kv8Cache& c, const Kv8Batch& bt, const
   a.ldq = ldq;
   a.q_heads = q_heads;
   a.group = q_heads / c.heads;
-  a.row_tiles = static_cast<int>((static_cast<int64_t>(bt.max_new) * a.group + kTcRows - 1) / kTcRows);
+  a.row_tiles = static_cast<int>((static_cast<int64_t>(bt.max_new) * a.group + 2 * kTcRows - 1) /
+                                 (2 * kTcRows));
   a.scale_log2 = scale * 1.4426950408889634f;
   if (fmt == kKvInt8)
     return D == 64 ? launch_tc<kKvInt8, 64>(a, stream, err) : launch_tc<kKvInt8, 128>(a, stream, err);
