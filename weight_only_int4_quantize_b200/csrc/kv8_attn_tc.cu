@@ -16,10 +16,11 @@
 //
 // Per row tile and 64 keys (D = 128) the tensor pipe needs 512 cycles (640
 // with the shared-memory reads of the score product) and the exponential unit
-// 512; what has to be kept out of the way is latency.  S is released once it
-// is in registers, so the next scores run under the exponentials; P has two
-// buffers, so a row tile's softmax never waits for its outputs; each row tile
-// has its own issuing warp, so one does not wait for the other's softmax.
+// 512; what has to be kept out of the way is latency.  Scores have two
+// buffers, and P takes the place of the scores that it was made of, so the
+// scores of the next tile lie ready while a tile's exponentials run and a row
+// tile's softmax never waits for its outputs; each row tile has its own
+// issuing warp, so one does not wait for the other's softmax.
 // 2 x 2048 tokens over up to 8192 keys, 16 / 8 heads: 128 rows per CTA and
 // two CTAs per SM 371 us; 256 rows, one issuing warp, codes fetched into
 // registers one tile ahead 340 us (with the fetches taken out 238 us, with
@@ -66,8 +67,9 @@ struct TcSmem {
   static constexpr size_t bytes = misc + 32 + 1024;
 };
 
-// TMEM columns: O and S of both row tiles, two P each (two fp16 per column).
-constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemP = 384, kTmemAll = 512;
+// TMEM columns: O of both row tiles, two S each (P, two fp16 per column, in
+// the first half of the S it replaces).
+constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemAll = 512;
 
 __device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -168,11 +170,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t bar = base + SM::bars;
   // One of each per row tile.
   auto q_full = [&](int t) { return bar + 8u * t; };
-  auto s_full = [&](int t) { return bar + 16u + 8u * t; };
-  auto s_empty = [&](int t) { return bar + 32u + 8u * t; };
-  // P has a barrier per buffer: a warp may be a key tile ahead of another (it
-  // needs only that all have read S), and its arrival must not count for the
-  // slower one's tile.
+  // S and P have a barrier per buffer: a softmax warp may be a key tile ahead
+  // of another, and its arrival must not count for the slower one's tile.
+  auto s_full = [&](int t, int buf) { return bar + 16u + 8u * (2 * t + buf); };
   auto p_full = [&](int t, int buf) { return bar + 48u + 8u * (2 * t + buf); };
   auto pv_done = [&](int t) { return bar + 80u + 8u * t; };
   auto done_bar = [&](int t) { return bar + 96u + 8u * t; };
@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 4);
-      mbar_init(s_full(t), 1);
-      mbar_init(s_empty(t), 4);
+      mbar_init(s_full(t, 0), 1);
+      mbar_init(s_full(t, 1), 1);
       mbar_init(p_full(t, 0), 4);
       mbar_init(p_full(t, 1), 4);
       mbar_init(pv_done(t), 1);
@@ -266,8 +266,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int64_t out_row = static_cast<int64_t>(s.row0 + tok) * a.q_heads + h * a.group +
                             (live ? r - tok * a.group : 0);
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t t_o = lane_addr + kTmemO + 128 * rtile, t_s = lane_addr + kTmemS + 64 * rtile,
-                   t_p = lane_addr + kTmemP + 64 * rtile;
+    const uint32_t t_o = lane_addr + kTmemO + 128 * rtile, t_s0 = lane_addr + kTmemS + 128 * rtile;
     float back = 0.f;  // undoes the query scaling, times the softmax scale
     if (my_tiles > 0) {
       // This row of Q, scaled by a power of two, into the swizzled tiles; a
@@ -331,16 +330,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool all_seen = tok0 + kKeys - 1 <= first_limit;  // by every live row
       const int seen = limit - tok0;  // columns 0 .. seen of the tile count
 
-      ok = mbar_wait(s_full(rtile), j & 1u, abort_flag, err, kKernelIdAttnTc);
+      const uint32_t t_s = t_s0 + 64 * (j & 1);
+      ok = mbar_wait(s_full(rtile, j & 1), (j >> 1) & 1u, abort_flag, err, kKernelIdAttnTc);
       if (!ok) break;
       tc_fence_after();
       uint32_t sc[2][32];
       tmem_ld32(t_s, sc[0]);
       tmem_ld32(t_s + 32, sc[1]);
       tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_empty(rtile));
 
       // Largest score; masked scores (which may be anything) do not count.
       float top = -INFINITY;
@@ -418,9 +415,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tmem_st32(t_o + c, o);
         }
       }
-      // This P buffer was read by the product before the last, which ended
-      // before the last one's scores were committed (s_full below).
-      tmem_st32(t_p + 32 * (j & 1), p);
+      tmem_st32(t_s, p);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -469,52 +464,54 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr uint32_t idesc_s = idesc_f16(kTcRows, kKeys, false);
     constexpr uint32_t idesc_o = idesc_f16(kTcRows, D, false);
     const int my_tiles = t ? tiles1 : tiles0;
-    const uint32_t t_s = tmem + kTmemS + 64 * t, t_o = tmem + kTmemO + 128 * t,
-                   t_p = tmem + kTmemP + 64 * t;
+    const uint32_t t_s0 = tmem + kTmemS + 128 * t, t_o = tmem + kTmemO + 128 * t;
     bool issued = false;
-    // Scores of key tile j (stage st, its phase ph).
-    auto scores = [&](int j, int st, uint32_t ph) {
-      if (!mbar_wait(k_full(st), ph, abort_flag, err, kKernelIdAttnTc)) return false;
-      if (j > 0 && !mbar_wait(s_empty(t), (j - 1) & 1u, abort_flag, err, kKernelIdAttnTc))
-        return false;
+    // Scores of key tile j, which come two by two ahead of the outputs: the
+    // buffer's last user, the outputs of tile j - 2, was issued before.
+    int kst = 0;
+    uint32_t kph = 0;
+    auto scores = [&](int j) {
+      if (!mbar_wait(k_full(kst), kph, abort_flag, err, kKernelIdAttnTc)) return false;
       tc_fence_after();
       if (one) {
 #pragma unroll
         for (int half = 0; half < kHalves; ++half) {
           const uint64_t da = sdesc_k_sw128(base + t * SM::kQ + half * (kTcRows * 128));
-          const uint64_t db = sdesc_k_sw128(base + SM::k + st * SM::kK + half * (kKeys * 128));
+          const uint64_t db = sdesc_k_sw128(base + SM::k + kst * SM::kK + half * (kKeys * 128));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_f16(t_s, da + 2ull * kk, db + 2ull * kk, idesc_s, (half | kk) != 0);
+            umma_f16(t_s0 + 64 * (j & 1), da + 2ull * kk, db + 2ull * kk, idesc_s,
+                     (half | kk) != 0);
         }
-        umma_commit(s_full(t));
-        umma_commit(k_empty(st));
+        umma_commit(s_full(t, j & 1));
+        umma_commit(k_empty(kst));
       }
       issued = true;
+      if (++kst == kTcStages) kst = 0, kph ^= 1u;
       return true;
     };
     bool ok = true;
-    if (my_tiles > 0)
-      ok = mbar_wait(q_full(t), 0, abort_flag, err, kKernelIdAttnTc) && scores(0, 0, 0);
-    int st = 0, nst = 1;
-    uint32_t ph = 0, nph = 0;
+    if (my_tiles > 0) {
+      ok = mbar_wait(q_full(t), 0, abort_flag, err, kKernelIdAttnTc) && scores(0);
+      if (ok && my_tiles > 1) ok = scores(1);
+    }
+    int st = 0;
+    uint32_t ph = 0;
     for (int j = 0; ok && j < my_tiles; ++j) {
-      // The next scores before this tile's outputs: they run under its softmax.
-      if (j + 1 < my_tiles && !scores(j + 1, nst, nph)) break;
-      if (!mbar_wait(v_full(st), ph, abort_flag, err, kKernelIdAttnTc)) break;
-      if (!mbar_wait(p_full(t, j & 1), (j >> 1) & 1u, abort_flag, err, kKernelIdAttnTc)) break;
+      ok = mbar_wait(v_full(st), ph, abort_flag, err, kKernelIdAttnTc) &&
+           mbar_wait(p_full(t, j & 1), (j >> 1) & 1u, abort_flag, err, kKernelIdAttnTc);
+      if (!ok) break;
       tc_fence_after();
       if (one) {
         const uint64_t db = sdesc_k_sw128(base + SM::v + st * SM::kV);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_f16_ta(t_o, t_p + 32 * (j & 1) + 8 * kk, db + 2ull * kk, idesc_o, (j | kk) != 0);
+          umma_f16_ta(t_o, t_s0 + 64 * (j & 1) + 8 * kk, db + 2ull * kk, idesc_o, (j | kk) != 0);
         umma_commit(pv_done(t));
         umma_commit(v_empty(st));
       }
-      st = nst;
-      ph = nph;
-      if (++nst == kTcStages) nst = 0, nph ^= 1u;
+      if (++st == kTcStages) st = 0, ph ^= 1u;
+      if (j + 2 < my_tiles) ok = scores(j + 2);
     }
     // Key tiles that only the other row tile has: release them as they come.
     for (int j = my_tiles; ok && j < tiles && !*abort_flag; ++j) {
