@@ -348,6 +348,32 @@ def test_attention_single_tokens_without_starts():
     assert torch.equal(a, p.check_attention())
 
 
+LONG = [  # heads, q_heads, d, page, lens, news: the tcgen05 kernel's problems
+    (16, 32, 64, 16, [300, 41], [260, 41]), (24, 48, 128, 64, [513, 255], [200, 255]),
+    (12, 36, 64, 128, [385, 128, 0, 77], [200, 128, 0, 77]), (20, 20, 128, 32, [700], [600]),
+    (12, 24, 128, 16, [100, 3, 260], [260, 3, 130]),  # some tokens in front of position 0
+]
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,q_heads,d,page,lens,news", LONG)
+def test_attention_long_runs(fmt, heads, q_heads, d, page, lens, news):
+    """Row tiles of which some warps have no live rows, key tiles that only
+    the second row tile has, maxima and value scales that move late (large
+    key scales, pages of very different scales)."""
+    p = Problem(fmt, heads, d, page, lens, news, q_heads, seed=sum(lens) + d, pad_rows=2)
+    for turn in range(2):
+        p.check_attention()
+        p.ks = p.ks * 4
+        p.vs = p.vs * 2.0 ** np.random.RandomState(turn).randint(-4, 5, p.vs.shape)
+
+
+def test_attention_negative_scale_and_strong_queries():
+    p = Problem("int8", 24, 64, 32, [400], [300], 48, seed=6)
+    p.check_attention(scale=-0.2)
+    p.check_attention(scale=0.0)
+
+
 @pytest.mark.parametrize("fmt", list(KV))
 def test_attention_scales_spread(fmt):
     """Pages whose value scales differ by 2^10 and key scales that make the

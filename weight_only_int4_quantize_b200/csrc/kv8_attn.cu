@@ -40,7 +40,6 @@
 // far and rounded to fp16 with a shift of 2^14 (the largest is 2^14, full
 // precision down to 2^-28 of it); sums and outputs are fp32.
 #include <cooperative_groups.h>
-#include <cstdlib>
 
 #include "kv8.cuh"
 #include "w4_kernels.h"
@@ -51,22 +50,30 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kAttnThreads = 32 * kWarps;
 constexpr int kTileTokens = 64;
-constexpr int kSlots = 3;  // ring slots per warp, alternately key and value tiles
 constexpr float kShift = 14.f;  // probabilities are kept times 2^14
 constexpr unsigned kKernelIdAttn = 32;
 
-template <int D>
-struct AttnSmem {
+// A launch's shape: 8 NT rows, W warps per CTA.  16 rows need some 210
+// registers, so two CTAs of four warps share an SM, with three ring slots
+// (alternately key and value tiles) per warp; 8 rows need 150, so three CTAs
+// do, or one of twelve warps where few problems leave one CTA per SM (a warp
+// alone on its scheduler waits for its own instructions: 32768 tokens of 8 kv
+// heads took 27 us with four warps per SM), with two slots.
+template <int D, int NT, int W>
+struct AttnShape {
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kCtasPerSm = W > 4 ? 1 : NT == 1 ? 3 : 2;
+  static constexpr int kSlots = NT == 1 ? 2 : 3;
   static constexpr int kSlotBytes = kTileTokens * D;
-  static constexpr int kRing = kWarps * kSlots * kSlotBytes;
+  static constexpr int kRing = W * kSlots * kSlotBytes;
   // Joined partial of the CTA (read by the cluster's peers), apart from the
   // ring: rows of D floats, then maxima and sums.
   static constexpr int part = kRing;
-  static constexpr int ml = part + 16 * D * 4;
+  static constexpr int ml = part + 8 * NT * D * 4;
   static constexpr int bytes = ml + 2 * 16 * 4;
+  // The warps' partials take the ring's place.
+  static_assert(W * 8 * NT * ((D + 4) * 4 + 8) <= kRing, "partials fit the ring");
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -107,10 +114,11 @@ struct AttnArgs {
   float scale_log2;  // softmax scale * log2(e)
 };
 
-template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, 2)
+template <int FMT, int D, int NT, int W>
+__global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
     kv8_attention_rows_kernel(const AttnArgs a, unsigned* err) {
-  using SM = AttnSmem<D>;
+  using SM = AttnShape<D, NT, W>;
+  constexpr int kWarps = W, kAttnThreads = 32 * W, kSlots = SM::kSlots;
   constexpr int kRows = 8 * NT;
   constexpr int kSteps = D / 16;    // k-steps of the score product
   constexpr int kChunks = D / 64;   // 16-byte pieces of a key row per lane
@@ -475,12 +483,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   cluster.sync();  // peers keep their partials until every reader is done
 }
 
-template <int FMT, int D, int NT>
-cudaError_t launch_rows(AttnArgs a, cudaStream_t stream, int num_sms, unsigned* err) {
-  using SM = AttnSmem<D>;
-  constexpr auto kern = kv8_attention_rows_kernel<FMT, D, NT>;
-  a.row_tiles = static_cast<int>((static_cast<int64_t>(a.bt.max_new) * a.group + 8 * NT - 1) /
-                                 (8 * NT));
+template <int FMT, int D, int NT, int W>
+cudaError_t launch_shape(AttnArgs a, int ks, cudaStream_t stream, unsigned* err) {
+  using SM = AttnShape<D, NT, W>;
+  constexpr auto kern = kv8_attention_rows_kernel<FMT, D, NT, W>;
   static unsigned long long done = 0;  // bit d: device d
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -493,16 +499,10 @@ cudaError_t launch_rows(AttnArgs a, cudaStream_t stream, int num_sms, unsigned* 
     if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELEASE);
   }
   const int64_t probs = static_cast<int64_t>(a.bt.batch) * a.c.heads * a.row_tiles;
-  // A problem's tiles are split over a cluster while the CTAs still fit the
-  // GPU at once; the table's width bounds the lengths.
-  const int64_t tiles = ((static_cast<int64_t>(a.bt.max_pages) << a.c.log_page) + kTileTokens - 1) /
-                        kTileTokens;
-  int ks = 1;
-  while (ks < 16 && ks * 2 * kWarps <= tiles && probs * ks * 2 <= 2 * num_sms) ks *= 2;
   if (probs * ks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(probs * ks), 1, 1);
-  cfg.blockDim = dim3(kAttnThreads, 1, 1);
+  cfg.blockDim = dim3(SM::kThreads, 1, 1);
   cfg.dynamicSmemBytes = SM::bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -517,12 +517,35 @@ cudaError_t launch_rows(AttnArgs a, cudaStream_t stream, int num_sms, unsigned* 
   return cudaLaunchKernelEx(&cfg, kern, a, err);
 }
 
+template <int FMT, int D, int NT>
+cudaError_t launch_rows(AttnArgs a, cudaStream_t stream, int num_sms, unsigned* err) {
+  a.row_tiles = static_cast<int>((static_cast<int64_t>(a.bt.max_new) * a.group + 8 * NT - 1) /
+                                 (8 * NT));
+  const int64_t probs = static_cast<int64_t>(a.bt.batch) * a.c.heads * a.row_tiles;
+  // A problem's tiles are split over a cluster while the CTAs still fit the
+  // GPU at once; the table's width bounds the lengths.
+  const int64_t tiles = ((static_cast<int64_t>(a.bt.max_pages) << a.c.log_page) + kTileTokens - 1) /
+                        kTileTokens;
+  auto split = [&](int warps, int64_t slots) {
+    int ks = 1;
+    while (ks < 16 && ks * 2 * warps <= tiles && probs * ks * 2 <= slots) ks *= 2;
+    return ks;
+  };
+  if constexpr (NT == 1) {
+    const int ks = split(12, num_sms);
+    if (probs * ks <= num_sms && tiles >= 24 * ks)
+      return launch_shape<FMT, D, NT, 12>(a, ks, stream, err);
+  }
+  const int ks = split(4, static_cast<int64_t>(AttnShape<D, NT, 4>::kCtasPerSm) * num_sms);
+  return launch_shape<FMT, D, NT, 4>(a, ks, stream, err);
+}
+
 }  // namespace
 
 cudaError_t launch_kv8_attention(const Kv8Cache& c, const Kv8Batch& bt, const void* q, int64_t ldq,
                                  int q_heads, int D, int fmt, float scale, void* out,
                                  cudaStream_t stream, int num_sms, unsigned* err) {
-  if (getenv("W4_TC") && kv8_attention_tc_fits(c, bt))
+  if (kv8_attention_prefers_tc(c, bt, q_heads / c.heads, num_sms))
     return launch_kv8_attention_tc(c, bt, q, ldq, q_heads, D, fmt, scale, out, stream, err);
   AttnArgs a;
   a.c = c;

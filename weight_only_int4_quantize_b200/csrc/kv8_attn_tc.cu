@@ -401,10 +401,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (all_seen) weights(std::false_type{}); else weights(std::true_type{});
       // O is moved between products: all up to the last tile's are done and
       // this tile's waits for P.
-      if (j > 0 && __any_sync(0xffffffffu, move_m || move_v)) {
+      // The last tile's product is waited for before the last P in any case:
+      // once that is there two more products may end, and a wait for the
+      // first of them would find its phase gone by.
+      const bool move = __any_sync(0xffffffffu, move_m || move_v);
+      if (j > 0 && (move || j == my_tiles - 1)) {
         ok = mbar_wait(pv_done(rtile), (j - 1) & 1u, abort_flag, err, kKernelIdAttnTc);
         if (!ok) break;
         tc_fence_after();
+      }
+      if (j > 0 && move) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -421,10 +427,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full(rtile, j & 1));
     }
-    // The last two products (the one before them ended before the last scores
-    // were committed), each phase in turn.
-    for (int j = my_tiles > 1 ? my_tiles - 2 : 0; ok && j < my_tiles; ++j)
-      ok = mbar_wait(pv_done(rtile), j & 1u, abort_flag, err, kKernelIdAttnTc);
+    if (ok && my_tiles > 0)
+      ok = mbar_wait(pv_done(rtile), (my_tiles - 1) & 1u, abort_flag, err, kKernelIdAttnTc);
     tc_fence_after();
     if (ok && rows_of(rtile) > 0) {
       // l is times 2^9 like P, so the factors cancel.
@@ -673,8 +677,19 @@ cudaError_t launch_tc(const TcArgs& a, cudaStream_t stream, unsigned* err) {
 
 }  // namespace
 
-bool kv8_attention_tc_fits(const Kv8Cache& c, const Kv8Batch& bt) {
-  return static_cast<int64_t>(bt.batch) * c.heads <= 65535;  // a grid axis
+// Which kernel: per 64 keys the tcgen05 kernel takes 1.2 us (one row tile) or
+// 1.95 us (two) for each wave of CTAs, the rows kernel about 0.003 us for each
+// 16 rows of each problem (whatever the lengths, which the host does not
+// know, they enter both alike).  Measured, rows / tcgen05 kernel: 8 x 128
+// tokens over 4096 keys (16 / 8 heads) 156 / 100 us, 8 x 64 90 / 78, 8 x 16
+// 35 / 76; 1 x 256 over 16384 205 / 360; 2 x 2048 over 8192 917 / 254.
+bool kv8_attention_prefers_tc(const Kv8Cache& c, const Kv8Batch& bt, int group, int num_sms) {
+  const int64_t problems = static_cast<int64_t>(bt.batch) * c.heads;
+  if (problems > 65535) return false;  // a grid axis
+  const int64_t rows = static_cast<int64_t>(bt.max_new) * group;
+  const double ctas = static_cast<double>(problems) * ((rows + 2 * kTcRows - 1) / (2 * kTcRows));
+  const double waves = ctas > num_sms ? ctas / num_sms : 1.0;
+  return waves * (rows > kTcRows ? 1.95 : 1.2) < 0.003 * ((rows + 15) / 16) * problems;
 }
 
 cudaError_t launch_kv8_attention_tc(const Kv8Cache& c, const Kv8Batch& bt, const void* q,

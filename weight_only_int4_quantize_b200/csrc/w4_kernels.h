@@ -249,7 +249,7 @@ cudaError_t launch_kv8_attention(const Kv8Cache& c, const Kv8Batch& bt, const vo
                                  int q_heads, int D, int fmt, float scale, void* out,
                                  cudaStream_t stream, int num_sms, unsigned* err);
 // The tcgen05 kernel for long runs of new tokens (kv8_attn_tc.cu).
-bool kv8_attention_tc_fits(const Kv8Cache& c, const Kv8Batch& bt);
+bool kv8_attention_prefers_tc(const Kv8Cache& c, const Kv8Batch& bt, int group, int num_sms);
 cudaError_t launch_kv8_attention_tc(const Kv8Cache& c, const Kv8Batch& bt, const void* q,
                                     int64_t ldq, int q_heads, int D, int fmt, float scale,
                                     void* out, cudaStream_t stream, unsigned* err);
