@@ -41,6 +41,8 @@
 // precision down to 2^-28 of it); sums and outputs are fp32.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "kv8.cuh"
 #include "w4_kernels.h"
 
@@ -89,6 +91,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -155,9 +163,10 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
   const int page_mask = (1 << a.c.log_page) - 1;
   const uint32_t ring = smem_u32(smem) + warp * (kSlots * SM::kSlotBytes) + lane * 16;
   bool bad_page = false;
-  // The page that holds 16-token granule `gr` of tile i, -1 if none does.
-  auto page_of = [&](int i, int gr) {
-    const int tok = (t_begin + warp + i * kWarps) * kTileTokens + 16 * gr;
+  // The page that holds the lane's granule (16 tokens) g / 2 of tile i, -1 if
+  // none does.  The value granule t of a lane is that of the lanes g = 2 t.
+  auto page_of = [&](int i) {
+    const int tok = (t_begin + warp + i * kWarps) * kTileTokens + 16 * (g >> 1);
     if (i >= my_tiles || tok >= keys) return -1;
     const int p = __ldg(table + (tok >> a.c.log_page));
     if (p < 0 || p >= a.c.num_pages) {
@@ -166,45 +175,54 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
     }
     return p;
   };
-  // Unit u: keys (even) or values (odd) of tile u / 2 into slot u % kSlots.
-  auto issue = [&](int u) {
-    const int i = u >> 1;
+  const int64_t page_bytes = (static_cast<int64_t>(a.c.heads) << a.c.log_page) * D;
+  const int64_t head_bytes = (static_cast<int64_t>(h) << a.c.log_page) * D;
+  const uint8_t* k_lane = a.c.k + head_bytes + (g & 1) * D + 16 * t;
+  const uint8_t* v_lane = a.c.v + head_bytes + (static_cast<int64_t>(g) << a.c.log_page);
+  const int64_t v_step = static_cast<int64_t>(8) << a.c.log_page;
+  // Unit u: keys (even) or values (odd) of tile u / 2, whose granule lies in
+  // `page`, into slot u % kSlots.
+  auto issue_k = [&](int i, int slot, int page) {
     if (i < my_tiles) {
-      const uint32_t dst = ring + (u % kSlots) * SM::kSlotBytes;
-      const int tok0 = (t_begin + warp + i * kWarps) * kTileTokens;
-      const int gr = (u & 1) ? t : g >> 1;
-      const int page = page_of(i, gr);
-      const int in_page = (tok0 + 16 * gr) & page_mask;
-      const int64_t head = (static_cast<int64_t>(page < 0 ? 0 : page) * a.c.heads + h)
-                           << a.c.log_page;
-      if (u & 1) {
-        // channels g, g + 8, g + 16, ... of the lane's 16 tokens
-        const uint8_t* src = a.c.v + head * D + in_page + (static_cast<int64_t>(g) << a.c.log_page);
+      const uint32_t dst = ring + slot * SM::kSlotBytes;
+      const int tok = (t_begin + warp + i * kWarps) * kTileTokens + 16 * (g >> 1);
+      // tokens g % 2, g % 2 + 2, + 4, ... of the granule
+      const uint8_t* src = k_lane + (page < 0 ? 0 : page) * page_bytes + (tok & page_mask) * D;
 #pragma unroll
-        for (int j = 0; j < 2 * kDTiles; ++j)
-          kv8_copy16(dst + j * 512, src + (static_cast<int64_t>(8 * j) << a.c.log_page), page >= 0);
-      } else {
-        // tokens g % 2, g % 2 + 2, + 4, ... of granule g / 2
-        const uint8_t* src = a.c.k + (head + in_page + (g & 1)) * D + 16 * t;
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            kv8_copy16(dst + (j * kChunks + c) * 512, src + 2 * j * D + 64 * c, page >= 0);
-      }
+        for (int c = 0; c < kChunks; ++c)
+          kv8_copy16(dst + (j * kChunks + c) * 512, src + 2 * j * D + 64 * c, page >= 0);
     }
     kv8_copy_commit();
   };
+  auto issue_v = [&](int i, int slot, int k_page) {
+    const int page = __shfl_sync(0xffffffffu, k_page, 8 * t);
+    if (i < my_tiles) {
+      const uint32_t dst = ring + slot * SM::kSlotBytes;
+      const int tok = (t_begin + warp + i * kWarps) * kTileTokens + 16 * t;
+      // channels g, g + 8, g + 16, ... of the lane's 16 tokens
+      const uint8_t* src = v_lane + (page < 0 ? 0 : page) * page_bytes + (tok & page_mask);
 #pragma unroll
-  for (int u = 0; u < kSlots; ++u) issue(u);
-  auto scales_of = [&](int i, float& sk, float& sv) {
-    const int p = page_of(i, g >> 1);
+      for (int j = 0; j < 2 * kDTiles; ++j, src += v_step)
+        kv8_copy16(dst + j * 512, src, page >= 0);
+    }
+    kv8_copy_commit();
+  };
+  // With two slots a tile's keys and values are on their way while it is
+  // waited for; with three also the next tile's keys.
+  int page = page_of(0), page_next = page_of(1);
+  issue_k(0, 0, page);
+  issue_v(0, 1, page);
+  if (kSlots > 2) issue_k(1, 2, page_next);
+  auto scales_of = [&](int p, float& sk, float& sv) {
     const int64_t at = static_cast<int64_t>(p < 0 ? 0 : p) * a.c.heads + h;
     sk = p < 0 ? 0.f : __ldg(a.c.ks + at);
     sv = p < 0 ? 0.f : __ldg(a.c.vs + at);
   };
   float sk_next, sv_next;
-  scales_of(0, sk_next, sv_next);
+  scales_of(page, sk_next, sv_next);
+  int slot_k = 0, slot_v = 1;  // of this tile
 
   // Query fragments: row 8 nt + g, scaled by a power of two.
   uint32_t qb[NT][kSteps][2];
@@ -267,7 +285,9 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
   for (int i = 0; i < my_tiles; ++i) {
     const int tok0 = (t_begin + warp + i * kWarps) * kTileTokens;
     const float sk = sk_next, sv = sv_next;
-    scales_of(i + 1, sk_next, sv_next);
+    page = page_next;  // of tile i + 1
+    page_next = page_of(i + 2);
+    scales_of(page, sk_next, sv_next);
     // ---- scores: sc[nt][i4][x], tokens 16 (g/2) + 4 i4 + g%2 (+ 2 for x >= 2)
     // of rows 2 t + x % 2 ----
     kv8_copy_wait<kSlots - 1>();
@@ -279,7 +299,7 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
 #pragma unroll
         for (int x = 0; x < 4; ++x) sc[nt][j][x] = 0.f;
     {
-      const uint32_t src = ring + ((2 * i) % kSlots) * SM::kSlotBytes;
+      const uint32_t src = ring + slot_k * SM::kSlotBytes;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         uint32_t kw[8][4];  // the lane's eight tokens
@@ -301,12 +321,12 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
           }
       }
     }
-    issue(2 * i + kSlots);
+    if (kSlots == 2) issue_k(i + 1, slot_k, page); else issue_v(i + 1, slot_k, page);
     // ---- online softmax ----
     const bool all_seen = tok0 + kTileTokens - 1 <= first_limit;
     float v_new = fmaxf(v_ref, column_max(sv));
-    const float v_old = v_new > 0.f ? v_ref / v_new : 0.f;
-    const float v_rel = v_new > 0.f ? sv / v_new : 0.f;
+    const float v_inv = v_new > 0.f ? __frcp_rn(v_new) : 0.f;
+    const float v_old = v_ref * v_inv, v_rel = sv * v_inv;
     v_ref = v_new;
     uint32_t pb[NT][4][2];
 #pragma unroll
@@ -317,19 +337,22 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
         const float f = q_back[nt][x] * sk;
         const int seen = limit[nt][x] - (tok0 + 16 * (g >> 1) + (g & 1));
         float top = -INFINITY;
+        auto scale_scores = [&](auto masks) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int hi = 0; hi < 2; ++hi) {
-            float v = sc[nt][j][2 * hi + x] * f;
-            // A masked score may be anything, so it is replaced, not added to.
-            if (!all_seen && 4 * j + 2 * hi > seen) v = -INFINITY;
-            sc[nt][j][2 * hi + x] = v;
-            top = fmaxf(top, v);
-          }
+            for (int hi = 0; hi < 2; ++hi) {
+              float v = sc[nt][j][2 * hi + x] * f;
+              // A masked score may be anything, so it is replaced, not added to.
+              if (decltype(masks)::value && 4 * j + 2 * hi > seen) v = -INFINITY;
+              sc[nt][j][2 * hi + x] = v;
+              top = fmaxf(top, v);
+            }
+        };
+        if (all_seen) scale_scores(std::false_type{}); else scale_scores(std::true_type{});
         const float mn = fmaxf(m[nt][x], column_max(top));
         const float at = mn == -INFINITY ? 0.f : mn;
-        keep[x] = exp2f(m[nt][x] - at);
+        keep[x] = ex2(m[nt][x] - at);
         m[nt][x] = mn;
         base[x] = at - kShift;
         l[nt][x] *= keep[x];
@@ -339,8 +362,8 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int hi = 0; hi < 2; ++hi) {
-          const float p0 = exp2f(sc[nt][j][2 * hi] - base[0]);
-          const float p1 = exp2f(sc[nt][j][2 * hi + 1] - base[1]);
+          const float p0 = ex2(sc[nt][j][2 * hi] - base[0]);
+          const float p1 = ex2(sc[nt][j][2 * hi + 1] - base[1]);
           l[nt][0] += p0;
           l[nt][1] += p1;
           const __half2 p = __floats2half2_rn(p0 * v_rel, p1 * v_rel);
@@ -354,7 +377,7 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
     // ---- outputs ----
     kv8_copy_wait<kSlots - 1>();
     {
-      const uint32_t src = ring + ((2 * i + 1) % kSlots) * SM::kSlotBytes;
+      const uint32_t src = ring + slot_v * SM::kSlotBytes;
       // Bytes behind the last key may hold anything, NaN codes included.
       const int held = keys - tok0 - 16 * t;  // tokens of this lane's 16 that count
       const bool ragged = tok0 + kTileTokens > keys;
@@ -366,18 +389,22 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
           const uint4 w = kv8_lds128(src + (2 * j0 + j) * 512);
           vw[j][0] = w.x, vw[j][1] = w.y, vw[j][2] = w.z, vw[j][3] = w.w;
         }
+        if (ragged) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int nb = held - 4 * x;  // bytes of this word that count
+            const uint32_t mask = nb >= 4 ? 0xFFFFFFFFu : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) vw[j][x] &= mask;
+          }
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          uint32_t mask = 0xFFFFFFFFu;
-          if (ragged) {
-            const int nb = held - 4 * x;  // bytes of this word that count
-            mask = nb >= 4 ? 0xFFFFFFFFu : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
-          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t f[4];
-            kv8_codes_to_f16<FMT>(vw[2 * j][x] & mask, f[0], f[2]);
-            kv8_codes_to_f16<FMT>(vw[2 * j + 1][x] & mask, f[1], f[3]);
+            kv8_codes_to_f16<FMT>(vw[2 * j][x], f[0], f[2]);
+            kv8_codes_to_f16<FMT>(vw[2 * j + 1][x], f[1], f[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(o[nt][j0 + j], f, pb[nt][x][0], pb[nt][x][1]);
@@ -385,7 +412,15 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
         }
       }
     }
-    issue(2 * i + 1 + kSlots);
+    if (kSlots == 2) {
+      issue_v(i + 1, slot_v, page);
+    } else {
+      issue_k(i + 2, slot_v, page_next);
+      // Unit u lies in slot u % 3.
+      const int was_k = slot_k;
+      slot_k = 3 - slot_k - slot_v;
+      slot_v = was_k;
+    }
   }
   kv8_copy_wait<0>();
   if (bad_page) record_error(err, kErrBadIndex, kKernelIdAttn);
@@ -434,7 +469,7 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(wm[w * kRows + row] - at);
+      const float f = ex2(wm[w * kRows + row] - at);
       sum += f * wm[(kWarps + w) * kRows + row];
       const float4 x = *reinterpret_cast<const float4*>(all_o + (w * kRows + row) * kLd + d);
       v.x += f * x.x;
@@ -469,7 +504,7 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p = 0; p < ks; ++p) {
       const float* ml = cluster.map_shared_rank(part_ml, p);
-      const float f = exp2f(ml[row] - at);
+      const float f = ex2(ml[row] - at);
       sum += f * ml[16 + row];
       const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, p) + row * D + d);
       v.x += f * x.x;
@@ -526,17 +561,19 @@ cudaError_t launch_rows(AttnArgs a, cudaStream_t stream, int num_sms, unsigned* 
   // GPU at once; the table's width bounds the lengths.
   const int64_t tiles = ((static_cast<int64_t>(a.bt.max_pages) << a.c.log_page) + kTileTokens - 1) /
                         kTileTokens;
-  auto split = [&](int warps, int64_t slots) {
+  auto split = [&](int most, int warps, int64_t slots) {
     int ks = 1;
-    while (ks < 16 && ks * 2 * warps <= tiles && probs * ks * 2 <= slots) ks *= 2;
+    while (ks < most && ks * 2 * warps <= tiles && probs * ks * 2 <= slots) ks *= 2;
     return ks;
   };
   if constexpr (NT == 1) {
-    const int ks = split(12, num_sms);
+    // Clusters of 16 such CTAs do not all fit their GPCs at one per SM (8
+    // clusters took two waves: 34 us where 8 CTAs each take 26).
+    const int ks = split(8, 12, num_sms);
     if (probs * ks <= num_sms && tiles >= 24 * ks)
       return launch_shape<FMT, D, NT, 12>(a, ks, stream, err);
   }
-  const int ks = split(4, static_cast<int64_t>(AttnShape<D, NT, 4>::kCtasPerSm) * num_sms);
+  const int ks = split(16, 4, static_cast<int64_t>(AttnShape<D, NT, 4>::kCtasPerSm) * num_sms);
   return launch_shape<FMT, D, NT, 4>(a, ks, stream, err);
 }
 
