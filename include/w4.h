@@ -643,13 +643,17 @@ w4_status w4_fp4_quantize(const void* x_bf16, int64_t R, int64_t K, int64_t ldx,
  * xcodes, xscales, xrow  x [M, K] as w4_fp4_quantize writes it.
  * wcodes, wscales, wrow  w [N, K] likewise (xrow, wrow: NULL iff W4_FP4_MX).
  * y_bf16     device bf16 [M, N] out.
- * flags      0 or W4_LINEAR_STATIC_WEIGHTS.  The kernel is always launched as
- *            a programmatic dependent launch; with the flag it may read the
- *            weight's codes and scales before the preceding kernel ends.
- * A weight tile is read once per 16, 32, 64, 128 or 256 tokens (the smallest
- * that holds M), K is split over a thread-block cluster of up to 8 CTAs when
- * there are few tiles; partial sums are added in a fixed order, so a call's
- * bits depend on its sizes and inputs alone.
+ * flags      0 or W4_LINEAR_STATIC_WEIGHTS.  The kernels of this section are
+ *            always launched as programmatic dependent launches and let the
+ *            next one be scheduled early; without the flag each touches memory
+ *            only after all work before it on the stream has ended.  With the
+ *            flag the linear may read the weight's codes and scales before
+ *            that: nothing still in flight on the stream may write them.
+ * A weight tile is read once per 16, 32, 64 or 128 tokens (the smallest that
+ * holds M), above once per 256 or 384 by pairs of CTAs; K is split over a
+ * thread-block cluster of up to 8 CTAs when there are few tiles.  Partial
+ * sums are added in a fixed order, so a call's bits depend on its sizes and
+ * inputs alone.
  */
 w4_status w4_fp4_linear(const uint8_t* xcodes, const uint8_t* xscales, const float* xrow, int64_t M,
                         const uint8_t* wcodes, const uint8_t* wscales, const float* wrow,
@@ -717,7 +721,11 @@ w4_status w4_kv8_append(const w4_kv8_cache* cache, const void* k_bf16, int64_t l
  *   out = softmax(scale * q . k) v,
  * query head h reading kv head h / (q_heads / kv_heads).  A token with p < 0
  * gets zeros.  Scores, sums and outputs in binary32; probabilities rounded to
- * fp16 (relative 2^-11), out once to bf16.
+ * fp16 (relative 2^-11; those under 2^-23 of the largest to a multiple of
+ * 2^-33 of it), out once to bf16.  Single tokens and short runs take a kernel
+ * that works on 8 or 16 rows (tokens x heads of a group) at a time and splits
+ * a sequence over a thread-block cluster of up to 16 CTAs; long runs take a
+ * tcgen05 kernel that works on 256 rows.
  *
  * q_bf16     device bf16 [rows, q_heads, head_dim], tokens ldq elements apart
  *            (a multiple of 8).

@@ -457,3 +457,212 @@ def test_decode_steps_together():
         oq = L.fp4_quantize(synth.bits(o.cpu().view(-1, hq * d)), fmt)[3]
         ry = oq @ ov.T
         assert np.all(np.abs(y.cpu().double().numpy() - ry) <= linear_bound(ry, oq, ov))
+
+
+# ------------------------------------------------------- bounds and hazards ----
+
+GUARD = 4096
+
+
+class Guarded:
+    """A tensor inside a byte buffer whose guard regions must stay untouched."""
+
+    def __init__(self, shape, dtype, fill=0x5A):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        self.raw = torch.full((GUARD + n + GUARD,), 0x5A, dtype=torch.uint8, device=DEV)
+        self.n = n
+        self.raw[GUARD: GUARD + n] = fill
+        self.t = self.raw[GUARD: GUARD + n].view(dtype).view(shape)
+
+    def check(self, what):
+        torch.cuda.synchronize()
+        assert bool((self.raw[:GUARD] == 0x5A).all()), f"{what}: write before the buffer"
+        assert bool((self.raw[GUARD + self.n:] == 0x5A).all()), f"{what}: write after the buffer"
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("r,k", [(1, 128), (37, 1152), (130, 5120)])
+def test_quantize_outputs_guarded(fmt, r, k):
+    x = synth.normal_activations(r, k, seed=r).to(DEV)
+    codes, scales = Guarded((r, k // 2), torch.uint8), Guarded(w4.fp4_scale_shape(r, k, fmt), torch.uint8)
+    row = Guarded((r,), torch.float32) if fmt == "nv" else None
+    values = Guarded((r, k), torch.bfloat16)
+    assert w4.lib().w4_fp4_quantize(x.data_ptr(), r, k, k, w4.FP4_FORMATS[fmt][0],
+                                    codes.t.data_ptr(), scales.t.data_ptr(),
+                                    row.t.data_ptr() if row else None, values.t.data_ptr(),
+                                    torch.cuda.current_stream().cuda_stream) == 0
+    for g, name in ((codes, "codes"), (scales, "scales"), (row, "row scales"), (values, "values")):
+        if g is not None:
+            g.check(name)
+    # bytes of rows behind the last are left as they were
+    last, used = scales.t[-1], r - (r - 1) // 128 * 128
+    i = torch.arange(used, 128, device=DEV)
+    for j in range(4):
+        assert bool((last[:, (i % 32) * 16 + i // 32 * 4 + j] == 0x5A).all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m,n,k", [(1, 77, 2048), (9, 129, 8192), (40, 130, 640), (100, 333, 2048),
+                                   (200, 140, 8192), (300, 520, 1152), (1000, 1025, 256)])
+def test_linear_output_guarded(fmt, m, n, k):
+    (wc, ws, wr), _ = fp4_weight(n, k, fmt, seed=2)
+    xc, xs, xr = w4.fp4_quantize(synth.normal_activations(m, k, seed=3).to(DEV), fmt)
+    y = Guarded((m, n), torch.bfloat16)
+    y.t.fill_(float("nan"))
+    w4.fp4_linear(xc, xs, xr, wc, ws, wr, fmt, out=y.t)
+    y.check(f"m={m} n={n} k={k}")
+    assert not bool(torch.isnan(y.t).any())
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,q_heads,d,page,lens,news", [
+    (2, 4, 64, 16, [40, 7, 0], [3, 7, 0]), (3, 3, 128, 64, [129, 200], [1, 90]),
+    (24, 48, 64, 32, [300, 50], [280, 20])])
+def test_cache_and_attention_guarded(fmt, heads, q_heads, d, page, lens, news):
+    """Appending writes nothing outside the cache, nor any page that no
+    sequence appends to; attention nothing outside its rows."""
+    p = Problem(fmt, heads, d, page, lens, news, q_heads, seed=11, pad_rows=2)
+    g = []
+    for t in p.cache():
+        x = Guarded(t.shape, t.dtype)
+        x.t.view(torch.uint8).copy_(t.view(torch.uint8))
+        g.append(x)
+    cache = w4.KV8Cache(*[x.t for x in g])
+    p.check_append(cache)  # compares whole buffers, other pages among them
+    out = Guarded((p.qkv.shape[0], q_heads, d), torch.bfloat16)
+    w4.kv8_attention(p.part(0, q_heads), cache, *p.batch(), out=out.t)
+    for x, name in zip(g + [out], ("k codes", "v codes", "k scales", "v scales", "out")):
+        x.check(name)
+    rows = int(p.starts[-1])
+    assert bool((out.t[rows:].view(torch.uint8) == 0x5A).all())
+
+
+@pytest.mark.parametrize("heads,news", [(2, [1, 3, 40]), (24, [1, 3, 300])])
+def test_bad_device_indexes_are_skipped_and_recorded(heads, news):
+    """Page ids, lengths and offsets outside the buffers: recorded in the
+    device error word, the other sequences unharmed, nothing written for them."""
+    lens = [33, 20, 310]
+    p = Problem("int8", heads, 64, 16, lens, news, heads, seed=5)
+    cache = p.cache()
+    good = p.check_attention(cache)
+    q, (table, ln, starts, most) = p.part(0, heads), p.batch()
+
+    def run(table=table, ln=ln, starts=starts):
+        before = [t.view(torch.uint8).clone() for t in cache]
+        w4.kv8_append(cache, q, q, table, ln, starts, most)
+        changed = [not torch.equal(a, t.view(torch.uint8)) for a, t in zip(before, cache)]
+        for a, t in zip(before, cache):
+            t.view(torch.uint8).copy_(a)
+        out = torch.full_like(good, 7.0)
+        w4.kv8_attention(q, cache, table, ln, starts, most, out=out)
+        torch.cuda.synchronize()
+        code = w4.device_error(clear=True)
+        assert code & 2 and not code & 1, code
+        return out, changed
+
+    def rows(b):
+        return slice(int(p.starts[b]), int(p.starts[b + 1]))
+
+    for bad in (-1, cache.k_codes.shape[0], 2 ** 31 - 1, -2 ** 31):
+        t = table.clone()
+        t[1, 0] = bad
+        out, _ = run(table=t)
+        assert torch.equal(out[rows(0)], good[rows(0)]) and torch.equal(out[rows(2)], good[rows(2)])
+    for bad in (-1, 16 * table.shape[1] + 1, 2 ** 31 - 1):
+        x = ln.clone()
+        x[1] = bad
+        out, _ = run(ln=x)
+        assert torch.equal(out[rows(0)], good[rows(0)]) and torch.equal(out[rows(2)], good[rows(2)])
+        assert bool((out[rows(1)] == 7.0).all())
+    x = starts.clone()
+    x[3] = q.shape[0] + 1  # the last sequence's rows run over the buffer
+    out, _ = run(starts=x)
+    assert torch.equal(out[rows(0)], good[rows(0)]) and bool((out[rows(2)] == 7.0).all())
+    x = starts.clone()
+    x[0] = -5
+    out, _ = run(starts=x)
+    assert torch.equal(out[rows(1)], good[rows(1)]) and torch.equal(out[rows(2)], good[rows(2)])
+    everything, changed = run(ln=torch.full_like(ln, -1))
+    assert bool((everything == 7.0).all()) and not any(changed)
+    with pytest.raises(w4.W4Error) as e:  # the status that the C ABI gives for it
+        w4.kv8_attention(q, cache, table, torch.full_like(ln, -1), starts, most)
+        torch.cuda.synchronize()
+        w4._check(w4.lib().w4_device_error(1, None), "w4_device_error")
+    assert e.value.name == "W4_ERR_DEVICE_INDEX"
+
+
+def test_pages_beyond_32_bit_offsets():
+    """Pages whose byte offsets pass 2^32, through each kernel."""
+    page, d = 128, 128
+    for heads, q_heads, lens, news in ((8, 16, [500, 200], [1, 1]), (8, 16, [500, 200], [1, 9]),
+                                       (24, 48, [300], [260])):
+        p = Problem("int8", heads, d, page, lens, news, q_heads, seed=9)
+        small = p.cache()
+        pages = 2 ** 32 // (heads * page * d) + 40
+        shift = pages - small.k_codes.shape[0]
+        big = w4.kv8_cache(pages, heads, page, d, device=DEV)
+        for b, s in zip(big, small):
+            b[shift:] = s
+        table, *rest = p.batch()
+        high = torch.where(table >= 0, table + shift, table)
+        for f in (lambda c, t: w4.kv8_append(c, p.part(q_heads, q_heads + heads),
+                                             p.part(q_heads + heads, q_heads + 2 * heads), t, *rest),
+                  lambda c, t: w4.kv8_attention(p.part(0, q_heads), c, t, *rest)):
+            a, b = f(small, table), f(big, high)
+            if a is not None:
+                assert torch.equal(a, b)
+        for b, s in zip(big, small):
+            assert torch.equal(b[shift:].view(torch.uint8), s.view(torch.uint8))
+            assert not bool(b[:shift].view(torch.uint8).any())
+        del big
+
+
+def test_more_than_32_bit_elements():
+    """Outputs and inputs of more than 2^31 elements: the last rows equal those
+    of a small call."""
+    for fmt in FMTS:
+        x = torch.randn(70000, 128, device=DEV).to(torch.bfloat16)
+        w = torch.randn(40000, 128, device=DEV).to(torch.bfloat16)
+        xq, wq = w4.fp4_quantize(x, fmt), w4.fp4_quantize(w, fmt)
+        y = w4.fp4_linear(*xq, *wq, fmt)
+        tail = w4.fp4_linear(*w4.fp4_quantize(x[69632:], fmt), *wq, fmt)  # a multiple of 128 rows
+        assert torch.equal(y[69632:], tail)
+        del y, tail
+    big = torch.zeros(150000, 16384, dtype=torch.bfloat16, device=DEV)
+    big[-300:] = torch.randn(300, 16384, device=DEV).to(torch.bfloat16)
+    for fmt in FMTS:
+        codes, scales, row = w4.fp4_quantize(big, fmt)
+        start = 149888 // 128 * 128
+        c2, s2, r2 = w4.fp4_quantize(big[start:], fmt)
+        assert torch.equal(codes[start:], c2)
+        assert torch.equal(scales[start // 128:, :, :16], s2[:, :, :16])  # rows 0, 32, 64, 96 ...
+        assert row is None or torch.equal(row[start:], r2)
+        del codes, scales
+
+
+def test_two_streams_at_once():
+    """The same operators on two streams, problems of different sizes
+    interleaved: nothing is shared between the calls."""
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    probs = []
+    for i, (m, n, k, fmt) in enumerate(((1, 2048, 4096, "mx"), (600, 1024, 2048, "nv"))):
+        (wc, ws, wr), _ = fp4_weight(n, k, fmt, seed=i)
+        x = synth.normal_activations(m, k, seed=50 + i).to(DEV)
+        p = Problem("int8", 4, 64, 16, [900, 40], [1, 1], 8, seed=i)
+        probs.append((x, wc, ws, wr, fmt, p, p.cache(), p.part(0, 8), p.batch(False)))
+    torch.cuda.synchronize()
+
+    def one(x, wc, ws, wr, fmt, p, cache, q, batch):
+        return w4.fp4_linear(*w4.fp4_quantize(x, fmt), wc, ws, wr, fmt), w4.kv8_attention(q, cache, *batch)
+
+    want = [one(*a) for a in probs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for s, a, g in zip(streams, probs, got):
+            with torch.cuda.stream(s):
+                g.append(one(*a))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for y, o in g:
+            assert torch.equal(y, w[0]) and torch.equal(o, w[1])
