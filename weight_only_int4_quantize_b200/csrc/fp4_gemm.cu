@@ -11,11 +11,11 @@
 // The weight is always the A operand and the tokens the B operand: up to 128
 // tokens a CTA takes 128 output channels x NB = 16 ... 128 token columns, so
 // a decode step streams the weight once through tiles of 16 columns; above,
-// two CTAs work on 256 channels x 256 or 384 tokens (pair kernel, below).  A stage is 256 channels: 128-byte rows of
-// codes (TMA, 128-byte swizzle) and 2 (mx) or 4 (nv) scale tiles of 512
-// bytes per 128 rows, copied to shared memory in one piece and to TMEM by
-// tcgen05.cp, which the tensor pipe runs in order with the MMAs.  A K tail
-// of 128 channels issues half the stage's MMAs.
+// two CTAs work on 256 channels x 256 or 384 tokens (pair kernel, below).  A
+// stage is 256 channels: 128-byte rows of codes (TMA, 128-byte swizzle) and 2
+// (mx) or 4 (nv) scale tiles of 512 bytes per 128 rows, copied to shared
+// memory in one piece and to TMEM by tcgen05.cp, which the tensor pipe runs in
+// order with the MMAs.  A K tail of 128 channels issues half the stage's MMAs.
 //
 // Warp roles: 0 TMA producer, 1 TMEM allocation and MMA issue, 2..5
 // epilogue.  K may be split over a thread-block cluster of up to 8 CTAs (few
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kFp4Threads)
 }
 
 // ---------------------------------------------------------------------------
-// Pair kernel (more than 256 tokens): a cluster of two CTAs computes a tile
+// Pair kernel (more than 128 tokens): a cluster of two CTAs computes a tile
 // of 256 output channels x NB tokens with cta_group::2 MMAs.  Each CTA holds
 // its 128 channels' codes and half of the tokens' codes, so a token tile is
 // fetched once for 256 channels.
@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(kFp4Threads)
 // 2 x 64 of 512 columns).
 //
 // Persistent: one pair per two SMs walks the tiles; the loads of the next
-// tile run under the epilogue of the last (the accumulators are single).
+// tile run under the epilogue of the last, and its MMAs under the stores (the
+// accumulators are single: they are handed back once they are in registers).
 //
 // Both CTAs' loads complete on the first CTA's barrier of the stage, whose
 // MMA warp issues for both (all loads are tensor-map loads, which may signal
@@ -422,8 +423,10 @@ __global__ void __launch_bounds__(kFp4Threads)
 // Issue order and uniformity matter as much as bandwidth: with the MMA loop
 // under `lane == 0` every tcgen05 operand went through a vector register and
 // one pair alone took 1.16 us per stage (NB = 384, nv); with the warp walking
-// the loop and an elected lane issuing, 0.62 us; with a relay thread passing
-// "stage full" to the first CTA replaced by direct signals, see below.
+// the loop and an elected lane issuing 0.62 us; with the loads signalling the
+// first CTA's barrier themselves, where a relaying thread of each CTA had
+// passed "stage full" on, 0.45 us (NB = 256: 0.30).  With every pair at work a
+// stage takes 0.57 (0.39) us: 8192 x 5120 x 17408 runs at 5.7 ... 5.9 PFLOP/s.
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 64 + 256;
 
@@ -737,33 +740,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       const bool ok = mbar_wait_cluster(acc_full, i & 1u, abort_flag, err);
       tc_fence_after();
       if (ok) {
-        const int c_end = half * (NB / 2) + NB / 2;
-#pragma unroll 1
-        for (int c = half * (NB / 2); c < c_end; c += 32) {
-          if (m0 + c >= a.M) break;
+        const int c0 = half * (NB / 2);
+        const int live = a.M - m0 - c0;  // columns that are tokens
+        uint16_t* dst = reinterpret_cast<uint16_t*>(a.y) + static_cast<int64_t>(m0 + c0) * a.N + n;
+        // Columns c0 + 32 j + 0 ... 31, rounded, two per word.
+        auto fetch = [&](int j, uint32_t offset, uint32_t* v) {
           uint32_t r[2][16];
-          tmem_ld_32x32b_x16(lane_addr + c, r[0]);
-          tmem_ld_32x32b_x16(lane_addr + c + 16, r[1]);
+          __syncwarp();
+          tmem_ld_32x32b_x16(lane_addr + c0 + 32 * j + offset, r[0]);
+          tmem_ld_32x32b_x16(lane_addr + c0 + 32 * j + 16 + offset, r[1]);
           tmem_ld_wait();
-          if (n < a.N) {
-            __nv_bfloat16* dst = a.y + static_cast<int64_t>(m0 + c) * a.N + n;
-            if (m0 + c + 32 <= a.M) {
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
-                dst[static_cast<int64_t>(x) * a.N] = __float2bfloat16_rn(
-                    __uint_as_float(r[x >> 4][x & 15]) * wr * xrow_s[c + x]);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (m0 + c + x < a.M)
-                  dst[static_cast<int64_t>(x) * a.N] = __float2bfloat16_rn(
-                      __uint_as_float(r[x >> 4][x & 15]) * wr * xrow_s[c + x]);
-            }
+          for (int x = 0; x < 16; ++x) {
+            const float2 xr = *reinterpret_cast<const float2*>(xrow_s + c0 + 32 * j + 2 * x);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(
+                __uint_as_float(r[x >> 3][2 * x & 15]) * wr * xr.x,
+                __uint_as_float(r[x >> 3][(2 * x & 15) + 1]) * wr * xr.y);
+            v[x] = *reinterpret_cast<const uint32_t*>(&y);
           }
+        };
+        auto store = [&](int j, const uint32_t* v) {
+          if (n >= a.N) return;
+          if (32 * j + 32 <= live) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x, dst += a.N)
+              *dst = static_cast<uint16_t>(v[x / 2] >> (16 * (x & 1)));
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x, dst += a.N)
+              if (32 * j + x < live) *dst = static_cast<uint16_t>(v[x / 2] >> (16 * (x & 1)));
+          }
+        };
+        if (i + 1 == my_tiles) {
+#pragma unroll 1
+          for (int j = 0; j < NB / 64 && 32 * j < live; ++j) {
+            uint32_t v[16];
+            fetch(j, 0, v);
+            store(j, v);
+          }
+        } else {
+          // All columns go to registers first and the accumulators are handed
+          // back before any of them is stored: the next tile's MMAs run under
+          // the stores (1999 x 11008 x 4096: 40.5 -> 38.2 us).
+          uint32_t held[NB / 64][16];
+          // 0, in a way that makes each read of 32 columns depend on the last
+          // one's results: read ahead, they would spill.
+          const uint32_t zero = static_cast<uint32_t>(a.M >> 31);
+          uint32_t order = 0;
+#pragma unroll
+          for (int j = 0; j < NB / 64; ++j) {
+            fetch(j, order & zero, held[j]);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) order |= held[j][x];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_at_first(acc_empty);
+#pragma unroll
+          for (int j = 0; j < NB / 64; ++j)
+            if (32 * j < live) store(j, held[j]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at_first(acc_empty);
       }
     }
   }
@@ -925,7 +961,7 @@ cudaError_t launch_pair(const uint8_t* xcodes, const uint8_t* wcodes, Fp4Args a,
 // per-stage cost + epilogue), plus the join of a split's partial tiles.
 // 5120 x 17408 at 200 tokens: pair 25.0, split 19.9; 11008 x 4096 at 200:
 // 10.7, 19.3; 8192 tokens x 5120 x 17408: 256 columns 263, 384 columns 249;
-// 1999 x 11008 x 4096: 43, 47.
+// 1999 x 11008 x 4096: 40, 47.
 int large_shape(int M, int N, int num_kb, int num_sms) {
   auto waves = [](int64_t tiles, int64_t slots) {
     return static_cast<double>((tiles + slots - 1) / slots);
