@@ -55,13 +55,13 @@ namespace {
 constexpr int kTileTokens = 64;
 constexpr float kShift = 14.f;  // probabilities are kept times 2^14
 constexpr unsigned kKernelIdAttn = 32;
+constexpr int kMaxSplit = 16;  // CTAs per cluster
 
 // A launch's shape: 8 NT rows, W warps per CTA.  16 rows need some 210
 // registers, so two CTAs of four warps share an SM, with three ring slots
 // (alternately key and value tiles) per warp; 8 rows need 150, so three CTAs
-// do, or one of twelve warps where few problems leave one CTA per SM (a warp
-// alone on its scheduler waits for its own instructions: 32768 tokens of 8 kv
-// heads took 27 us with four warps per SM), with two slots.
+// do, or one of twelve warps where few long problems leave one CTA per SM (a
+// warp alone on its scheduler waits for its own instructions), with two slots.
 template <int D, int NT, int W>
 struct AttnShape {
   static constexpr int kThreads = 32 * W;
@@ -519,37 +519,104 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
 }
 
 template <int FMT, int D, int NT, int W>
-cudaError_t launch_shape(AttnArgs a, int ks, cudaStream_t stream, unsigned* err) {
-  using SM = AttnShape<D, NT, W>;
+void set_cluster(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int64_t ctas, int ks) {
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(AttnShape<D, NT, W>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = AttnShape<D, NT, W>::bytes;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ks;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+}
+
+// Clusters of each size that the device holds at once (clusters do not pack
+// its GPCs evenly: 148 SMs hold 15 clusters of 8 or 9 CTAs, 11 of 10 and 7 of
+// 16 at one CTA per SM).  Asked for once per device; also where the kernel's
+// attributes are set.
+struct Fit {
+  int clusters[kMaxSplit + 1];
+};
+template <int FMT, int D, int NT, int W>
+cudaError_t clusters_at_once(Fit& fit) {
   constexpr auto kern = kv8_attention_rows_kernel<FMT, D, NT, W>;
-  static unsigned long long done = 0;  // bit d: device d
+  constexpr int kDevices = 64;
+  static Fit known[kDevices];
+  static int state[kDevices];  // 2: known (every thread that asks finds the same)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::bytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELEASE);
+  if (dev < kDevices && __atomic_load_n(&state[dev], __ATOMIC_ACQUIRE) == 2) {
+    fit = known[dev];
+    return cudaSuccess;
   }
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           AttnShape<D, NT, W>::bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  fit.clusters[0] = 0;
+  for (int ks = 1; ks <= kMaxSplit && e == cudaSuccess; ++ks) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    set_cluster<FMT, D, NT, W>(cfg, attr, ks, ks);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&fit.clusters[ks], kern, &cfg);
+  }
+  if (e != cudaSuccess) return e;
+  int none = 0;
+  if (dev < kDevices && __atomic_compare_exchange_n(&state[dev], &none, 1, false,
+                                                    __ATOMIC_ACQ_REL, __ATOMIC_RELAXED)) {
+    known[dev] = fit;
+    __atomic_store_n(&state[dev], 2, __ATOMIC_RELEASE);
+  }
+  return cudaSuccess;
+}
+
+// The split of K for W warps per CTA that takes the least time by a model in
+// microseconds, fitted to launches of 8 ... 1024 problems of 5 ... 1024 tiles
+// (within 25 %): waves x (start, join and per-tile rounds of a warp), a round
+// taking longer the more warps share an SM and the more SMs are at work.
+// 8 problems x 512 tiles: 16 x 4 warps 25.3 us, 8 x 12 25.5, 10 x 12 23.1;
+// x 32 tiles: 8 x 4 7.8, 4 x 12 8.5; 256 problems x 64: 1 x 4 48, 2 x 4 42.
+// Waves count in parts where an SM takes several CTAs (lengths differ, so
+// they end at different times), in full where it takes one.
+template <int NT, int W>
+double best_split(const Fit& fit, int64_t probs, int64_t tiles, int num_sms, int& best) {
+  double least = 0;
+  best = 0;
+  for (int ks = 1; ks <= kMaxSplit; ++ks) {
+    if (ks > 1 && (ks - 1) * W >= tiles) break;
+    if (fit.clusters[ks] < 1) continue;
+    const int64_t at_once = probs < fit.clusters[ks] ? probs : fit.clusters[ks];
+    const double per_sm = static_cast<double>(at_once * ks) / num_sms;
+    double waves = static_cast<double>(probs) / fit.clusters[ks];
+    if (W > 4) waves = static_cast<double>((probs + fit.clusters[ks] - 1) / fit.clusters[ks]);
+    if (waves < 1) waves = 1;
+    const double round = (NT == 1 ? 1. : 1.3) * (0.75 + 0.19 * W * (per_sm > 1 ? per_sm : 1) +
+                                                 0.65 * (per_sm < 1 ? per_sm : 1));
+    const double t = waves * ((ks == 1 ? 3. : 5.2 + 0.12 * ks) +
+                              round * (static_cast<double>(tiles) / (ks * W) + 0.5));
+    if (best == 0 || t < least) {
+      least = t;
+      best = ks;
+    }
+  }
+  return least;
+}
+
+template <int FMT, int D, int NT, int W>
+cudaError_t launch_shape(const AttnArgs& a, int ks, cudaStream_t stream, unsigned* err) {
   const int64_t probs = static_cast<int64_t>(a.bt.batch) * a.c.heads * a.row_tiles;
-  if (probs * ks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (ks < 1 || probs * ks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(probs * ks), 1, 1);
-  cfg.blockDim = dim3(SM::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = SM::bytes;
-  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
+  set_cluster<FMT, D, NT, W>(cfg, attr[1], probs * ks, ks);
+  cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ks;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, err);
+  return cudaLaunchKernelEx(&cfg, kv8_attention_rows_kernel<FMT, D, NT, W>, a, err);
 }
 
 template <int FMT, int D, int NT>
@@ -557,23 +624,21 @@ cudaError_t launch_rows(AttnArgs a, cudaStream_t stream, int num_sms, unsigned* 
   a.row_tiles = static_cast<int>((static_cast<int64_t>(a.bt.max_new) * a.group + 8 * NT - 1) /
                                  (8 * NT));
   const int64_t probs = static_cast<int64_t>(a.bt.batch) * a.c.heads * a.row_tiles;
-  // A problem's tiles are split over a cluster while the CTAs still fit the
-  // GPU at once; the table's width bounds the lengths.
+  // The table's width bounds the lengths.
   const int64_t tiles = ((static_cast<int64_t>(a.bt.max_pages) << a.c.log_page) + kTileTokens - 1) /
                         kTileTokens;
-  auto split = [&](int most, int warps, int64_t slots) {
-    int ks = 1;
-    while (ks < most && ks * 2 * warps <= tiles && probs * ks * 2 <= slots) ks *= 2;
-    return ks;
-  };
+  Fit fit;
+  cudaError_t e = clusters_at_once<FMT, D, NT, 4>(fit);
+  if (e != cudaSuccess) return e;
+  int ks;
+  const double four = best_split<NT, 4>(fit, probs, tiles, num_sms, ks);
   if constexpr (NT == 1) {
-    // Clusters of 16 such CTAs do not all fit their GPCs at one per SM (8
-    // clusters took two waves: 34 us where 8 CTAs each take 26).
-    const int ks = split(8, 12, num_sms);
-    if (probs * ks <= num_sms && tiles >= 24 * ks)
-      return launch_shape<FMT, D, NT, 12>(a, ks, stream, err);
+    e = clusters_at_once<FMT, D, NT, 12>(fit);
+    if (e != cudaSuccess) return e;
+    int ks12;
+    if (best_split<NT, 12>(fit, probs, tiles, num_sms, ks12) < four && ks12 > 0)
+      return launch_shape<FMT, D, NT, 12>(a, ks12, stream, err);
   }
-  const int ks = split(16, 4, static_cast<int64_t>(AttnShape<D, NT, 4>::kCtasPerSm) * num_sms);
   return launch_shape<FMT, D, NT, 4>(a, ks, stream, err);
 }
 
