@@ -124,7 +124,9 @@ def linear_bound(ref, xv, wv):
     (17, 300, 2176), (32, 256, 128), (33, 64, 896), (64, 333, 1024), (65, 130, 256),
     (128, 260, 512), (129, 128, 384), (200, 515, 1152), (256, 1001, 256), (257, 96, 128),
     (300, 384, 4096), (513, 2049, 640), (1, 5120, 17408), (13, 640, 17408), (1999, 200, 512),
-    (400, 130, 384), (769, 300, 640), (385, 1, 128), (1152, 512, 2048)])
+    (400, 130, 384), (769, 300, 640), (385, 1, 128), (1152, 512, 2048),
+    # several tiles for each pair of SMs: 256 and 384 token columns
+    (1999, 2951, 384), (2300, 4300, 1536)])
 def test_linear(fmt, m, n, k):
     (wc, ws, wr), wv = fp4_weight(n, k, fmt, seed=n + k)
     x = synth.normal_activations(m, k, seed=m + 3)

@@ -23,8 +23,12 @@
 // an mx block takes one shuffle, of an nv block none.  The four scale bytes
 // of a tile word are gathered by shuffles and stored as one word.  The nv
 // row maximum is a first pass over the row, which stays in registers: a row's
-// CTA has as many warps as it takes at one or two pieces per thread (8192 x
-// 17408: 140 us with 256 threads whatever the row, 4 or 5 pieces each).
+// CTA has as many warps as it takes at one to three pieces per thread (8192 x
+// 17408: 69 us, 5.2 TB/s, with 384 threads of three pieces, two CTAs per SM;
+// 83 with 544 of two and one CTA; 140 with 256 threads whatever the row).  mx
+// with values runs at 97 % of the copy rate (17408 x 5120: 63 us).
+#include <type_traits>
+
 #include "fp4.cuh"
 #include "w4_kernels.h"
 
@@ -158,10 +162,12 @@ __global__ void __launch_bounds__(kQuantThreads)
   }
 }
 
+constexpr int nv_registers(int held) { return held == 1 ? 48 : held == 2 ? 64 : 80; }
+
 // nv: a warp (WARP) or the CTA owns one row; a thread keeps HELD pieces in
 // registers between the passes (the rest of a longer row is read again).
 template <bool VALUES, bool WARP, int HELD>
-__global__ void __maxnreg__(HELD == 1 ? 48 : 64)
+__global__ void __maxnreg__(nv_registers(HELD))
     fp4_quantize_nv_kernel(const __nv_bfloat16* __restrict__ x, int64_t rows, int per_row,
                            int64_t ldx, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                            float* __restrict__ row_scale, __nv_bfloat16* __restrict__ values) {
@@ -286,17 +292,20 @@ cudaError_t quantize(const __nv_bfloat16* x, int64_t R, int64_t K, int64_t ldx, 
     return launch_pdl<fp4_quantize_nv_kernel<VALUES, true, 2>>(
         grid, kQuantThreads, stream, x, R, per_row, ldx, codes, scales, row_scale, values);
   }
-  // One piece per thread up to 512 threads (few rows: the latency of one
-  // round), then two; as many CTAs as are resident at once.
-  const int pieces = per_row <= 512 ? per_row : (per_row + 1) / 2;
-  const int threads = pieces < 1024 ? (pieces + 31) & ~31 : 1024;
-  const int64_t most = int64_t{num_sms} * (65536 / ((per_row <= 512 ? 48 : 64) * threads));
-  const int64_t grid = R < most ? R : most;
-  return per_row <= 512
-             ? launch_pdl<fp4_quantize_nv_kernel<VALUES, false, 1>>(
-                   grid, threads, stream, x, R, per_row, ldx, codes, scales, row_scale, values)
-             : launch_pdl<fp4_quantize_nv_kernel<VALUES, false, 2>>(
-                   grid, threads, stream, x, R, per_row, ldx, codes, scales, row_scale, values);
+  // Pieces per thread: one up to 512 threads (few rows: the latency of one
+  // round), else two, but three where two would leave one CTA of some 20 warps
+  // per SM and three make two CTAs fit; as many CTAs as are resident at once.
+  auto launch = [&](auto held) {
+    constexpr int kHeld = decltype(held)::value;
+    const int pieces = (per_row + kHeld - 1) / kHeld;
+    const int threads = pieces < 1024 ? (pieces + 31) & ~31 : 1024;
+    const int64_t most = int64_t{num_sms} * (65536 / (nv_registers(kHeld) * threads));
+    return launch_pdl<fp4_quantize_nv_kernel<VALUES, false, kHeld>>(
+        R < most ? R : most, threads, stream, x, R, per_row, ldx, codes, scales, row_scale, values);
+  };
+  if (per_row <= 512) return launch(std::integral_constant<int, 1>{});
+  if (per_row <= 1024 || per_row > 1152) return launch(std::integral_constant<int, 2>{});
+  return launch(std::integral_constant<int, 3>{});
 }
 
 }  // namespace

@@ -23,8 +23,11 @@
 // issuing warp, so one does not wait for the other's softmax.
 // 2 x 2048 tokens over up to 8192 keys, 16 / 8 heads: 128 rows per CTA and
 // two CTAs per SM 371 us; 256 rows, one issuing warp, codes fetched into
-// registers one tile ahead 340 us (with the fetches taken out 238 us, with
-// all but the handshakes taken out 163 us).
+// registers one tile ahead 340 us; an issuing warp per row tile and copies
+// three tiles ahead 260 us; two S buffers with P in place 252 us, 0.6 PFLOP/s
+// (28 % of the tensor pipe).  What is left is the softmax arithmetic of eight
+// warps, two per scheduler: 128-key tiles took 353 us, 128 us without that
+// arithmetic; 16 softmax warps of half a row each 381 us.
 //
 // Numerics as in the rows kernel (kv8_attn.cu): codes are exact in fp16; a
 // query row is scaled by a power of two; key scales (one per 16 keys at the
