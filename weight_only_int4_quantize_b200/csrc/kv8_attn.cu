@@ -143,6 +143,17 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
   const int h = bh % a.c.heads, b = bh / a.c.heads;
   pdl_launch_dependents();
   pdl_wait();
+  const int32_t* table = a.bt.table + static_cast<int64_t>(b) * a.bt.max_pages;
+  // Without a split a warp's first two tiles do not depend on the length:
+  // their page ids are read along with it (and used if it reaches there).
+  int first[2] = {-1, -1};
+  if (ks == 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t at = ((warp + i * kWarps) * kTileTokens + 16 * (g >> 1)) >> a.c.log_page;
+      if (at < a.bt.max_pages) first[i] = __ldg(table + at);
+    }
+  }
   const Kv8Seq s = kv8_sequence(a.bt, b, a.c.log_page);
   if (s.bad && threadIdx.x == 0 && h == 0 && rt == 0 && rank == 0)
     record_error(err, kErrBadIndex, kKernelIdAttn);
@@ -159,16 +170,15 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
   const int t_end = static_cast<int>(static_cast<int64_t>(rank + 1) * tiles / ks);
   const int my_tiles = t_end - t_begin > warp ? (t_end - t_begin - warp + kWarps - 1) / kWarps : 0;
 
-  const int32_t* table = a.bt.table + static_cast<int64_t>(b) * a.bt.max_pages;
   const int page_mask = (1 << a.c.log_page) - 1;
   const uint32_t ring = smem_u32(smem) + warp * (kSlots * SM::kSlotBytes) + lane * 16;
   bool bad_page = false;
   // The page that holds the lane's granule (16 tokens) g / 2 of tile i, -1 if
   // none does.  The value granule t of a lane is that of the lanes g = 2 t.
-  auto page_of = [&](int i) {
+  auto page_of = [&](int i, bool read = true, int p = 0) {
     const int tok = (t_begin + warp + i * kWarps) * kTileTokens + 16 * (g >> 1);
     if (i >= my_tiles || tok >= keys) return -1;
-    const int p = __ldg(table + (tok >> a.c.log_page));
+    if (read) p = __ldg(table + (tok >> a.c.log_page));
     if (p < 0 || p >= a.c.num_pages) {
       bad_page = true;
       return -1;
@@ -211,7 +221,7 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
   };
   // With two slots a tile's keys and values are on their way while it is
   // waited for; with three also the next tile's keys.
-  int page = page_of(0), page_next = page_of(1);
+  int page = page_of(0, ks > 1, first[0]), page_next = page_of(1, ks > 1, first[1]);
   issue_k(0, 0, page);
   issue_v(0, 1, page);
   if (kSlots > 2) issue_k(1, 2, page_next);
