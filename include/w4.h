@@ -621,6 +621,8 @@ size_t w4_fp4_scale_bytes(int64_t R, int64_t K, int format);
  *
  * x_bf16     device bf16 [R, K], rows ldx elements apart (ldx >= K, a
  *            multiple of 8).  1 <= R <= 2^31-1, K a positive multiple of 128.
+ *            Finite: codes and scales of a row (mx: a block) that holds an
+ *            infinity or NaN have no meaning; others are not affected.
  * codes_out  device uint8 [R, K/2] out.
  * scales_out device, w4_fp4_scale_bytes(R, K, format) bytes out.
  * row_scale_out  device float32 [R] out; NULL iff W4_FP4_MX.
@@ -700,7 +702,9 @@ typedef struct {
  *
  * k_bf16, v_bf16  device bf16 [rows, kv_heads, head_dim], tokens ldk / ldv
  *            elements apart (multiples of 8): slices of a fused projection's
- *            output can be passed as they are.
+ *            output can be passed as they are.  Finite: a page, kv head and
+ *            side that takes an infinity or NaN has no meaning; others are not
+ *            affected.
  * page_table device int32 [batch, max_pages].
  * seq_lens   device int32 [batch]: tokens in the cache after this call.
  * starts     device int32 [batch + 1]: sequence b's new tokens are rows

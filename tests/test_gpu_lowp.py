@@ -21,6 +21,10 @@ Bars:
     of that (the normalizer is at least the largest probability, 1 in these
     units).
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -668,3 +672,98 @@ def test_two_streams_at_once():
     for w, g in zip(want, got):
         for y, o in g:
             assert torch.equal(y, w[0]) and torch.equal(o, w[1])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_keeps_infinities_to_their_row(fmt, bad):
+    x = synth.normal_activations(200, 512, seed=8)
+    clean = w4.fp4_quantize(x.to(DEV), fmt)
+    x[77, 100] = bad
+    codes, scales, row = w4.fp4_quantize(x.to(DEV), fmt)
+    keep = np.arange(200) != 77
+    assert np.array_equal(codes.cpu().numpy()[keep], clean[0].cpu().numpy()[keep])
+    blocks = 512 // (32 if fmt == "mx" else 16)
+    r, b = np.meshgrid(np.arange(200)[keep], np.arange(blocks), indexing="ij")
+    at = (r // 128, b // 4, (r % 32) * 16 + (r % 128) // 32 * 4 + b % 4)
+    assert np.array_equal(scales.cpu().numpy()[at], clean[1].cpu().numpy()[at])
+    if row is not None:
+        assert np.array_equal(row.cpu().numpy()[keep], clean[2].cpu().numpy()[keep])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_append_keeps_infinities_to_their_page(fmt, bad):
+    dtype = torch.int8 if fmt == "int8" else torch.float8_e4m3fn
+    table = torch.arange(6, dtype=torch.int32, device=DEV).view(2, 3)
+    lens = torch.tensor([40, 35], dtype=torch.int32, device=DEV)
+    starts = torch.tensor([0, 40, 75], dtype=torch.int32, device=DEV)
+    k = synth.normal_activations(75, 2 * 64, seed=9).view(75, 2, 64).to(DEV)
+    v = synth.normal_activations(75, 2 * 64, seed=10).view(75, 2, 64).to(DEV)
+    caches = []
+    for spoilt in (False, True):
+        if spoilt:  # sequence 0, token 20 (page 1), kv head 1
+            k[20, 1, 5] = bad
+            v[20, 1, 6] = bad
+        cache = w4.kv8_cache(6, 2, 16, 64, dtype, DEV)
+        w4.kv8_append(cache, k, v, table, lens, starts, 40)
+        caches.append([c.view(torch.uint8).cpu() if c.element_size() == 1 else c.cpu() for c in cache])
+    for a, b in zip(*caches):
+        a[1, 1] = 0
+        b[1, 1] = 0
+        assert torch.equal(a, b)
+    assert w4.device_error() == 0
+
+
+FIRST_CALLS = """
+import torch
+import weight_only_int4_quantize_b200 as w4
+w4.lib()
+dev = "cuda:0"
+torch.manual_seed(0)
+stream = torch.cuda.Stream()
+x = torch.randn(300, 512, device=dev).bfloat16()
+w = torch.randn(384, 512, device=dev).bfloat16()
+k = torch.randn(4, 2, 128, device=dev).bfloat16()
+q = torch.randn(4, 4, 128, device=dev).bfloat16()
+long_q = torch.randn(300, 4, 128, device=dev).bfloat16()
+long_k = torch.randn(300, 2, 128, device=dev).bfloat16()
+table = torch.arange(4 * 128, dtype=torch.int32, device=dev).view(4, 128)
+lens = torch.tensor([2000, 7, 300, 1], dtype=torch.int32, device=dev)
+one = torch.tensor([300], dtype=torch.int32, device=dev)
+ends = torch.tensor([0, 300], dtype=torch.int32, device=dev)
+cache, other = w4.kv8_cache(512, 2, 16, 128), w4.kv8_cache(512, 2, 16, 128)
+
+def run(cache):
+    W = w4.fp4_quantize(w, "nv")
+    X = w4.fp4_quantize(x, "nv")
+    y = w4.fp4_linear(*X, *W, "nv")
+    z = w4.fp4_linear(*w4.fp4_quantize(x[:3], "mx"), *w4.fp4_quantize(w, "mx"), "mx")
+    w4.kv8_append(cache, long_k, long_k, table[2:3], one, ends, 300)
+    w4.kv8_append(cache, k, k, table, lens)
+    return y, z, w4.kv8_attention(q, cache, table, lens), \
+        w4.kv8_attention(long_q, cache, table[2:3], one, ends, 300)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=stream):
+    got = run(cache)
+graph.replay()
+graph.replay()
+torch.cuda.synchronize()
+want = run(other)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(cache, other))
+assert w4.device_error() == 0
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """No call needs a warm-up before it is captured into a graph, and a
+    replayed append leaves what one call leaves."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stdout + r.stderr
