@@ -1,9 +1,10 @@
 """Oracle of the microscaled 4-bit linear and of the 8-bit paged KV cache.
 
-Plain numpy in binary64, from the definitions in include/w4.h.  Scales of few
-significant bits make every quotient that decides a rounding either exactly on
-a border or at least 2^-16 (relative) away from it, so binary64 decides them
-exactly.  Shares no code with the CUDA side.
+Plain numpy in binary64, from the definitions in include/w4.h.  A quotient
+that decides a rounding is either exactly on a border or, with scales of 8
+significant bits, at least 2^-17 (relative) away from it, with any binary32
+scales at least 2^-33, so binary64 decides them exactly.  Shares no code with
+the CUDA side.
 """
 from __future__ import annotations
 

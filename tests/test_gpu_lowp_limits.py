@@ -1,0 +1,82 @@
+"""GPU tests of the microscaled and 8-bit KV cache operators at the ends of
+what their contracts allow.
+
+Appending is bit-exact against the binary64 oracle.
+"""
+import numpy as np
+import pytest
+import torch
+
+import weight_only_int4_quantize_b200 as w4
+from oracle import lowp_oracle as L
+from tests.test_gpu_lowp import KV, Problem
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    yield
+    torch.cuda.synchronize()
+    assert w4.device_error(clear=True) == 0
+
+
+# ------------------------------------------------------- foreign cache scales ----
+
+def foreign_scales(p, seed, low, high):
+    """Scales of 24 significant bits, log-uniform between low and high."""
+    r = np.random.RandomState(seed)
+    for name in ("ks", "vs"):
+        s = np.exp(r.uniform(np.log(low), np.log(high), getattr(p, name).shape))
+        setattr(p, name, s.astype(np.float32).astype(np.float64))
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,d,page,lens,news", [
+    (8, 128, 128, [100, 228, 64, 1000], [50, 60, 1, 30]), (4, 64, 16, [9, 31, 200, 17], [1, 3, 11, 8]),
+    (2, 128, 64, [40] * 6, [1] * 6), (3, 64, 32, [70, 31, 96], [35, 30, 90])])
+def test_append_into_pages_of_foreign_scales(fmt, heads, d, page, lens, news):
+    """Scales that this operator did not write have up to 24 significant bits:
+    quotients come closer to a rounding border than with its own 8-bit ones.
+    Half of the scales are larger than the new tokens need, so they stay and
+    the new codes are quotients by them; half are smaller, so the earlier codes
+    are products with them."""
+    p = Problem(fmt, heads, d, page, lens, news, q_heads=heads, seed=sum(lens) + d)
+    need = 4.5 / L.QMAX[fmt]  # about the largest of some thousand normal values
+    foreign_scales(p, d + page, need / 8, need * 8)
+    p.check_append()
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+def test_append_near_ties_of_foreign_scales(fmt):
+    """Scales chosen so that a new token's quotient misses a border by one
+    unit in the last place of the scale, on either side."""
+    heads = 16
+    p = Problem(fmt, heads, 64, 16, [5], [1], q_heads=heads, seed=3)
+    r = np.random.RandomState(5)
+    x = r.randint(128, 256, (heads, 64)) / 128.0
+    border = {"int8": r.randint(40, 120, heads) + 0.5,
+              "e4m3": (r.randint(8, 16, heads) + 0.5) * 8}[fmt]
+    page = p.table[0, 0]
+    for name in ("ks", "vs"):
+        s = (x[:, 0] / border).astype(np.float32)
+        s = np.where(np.arange(heads) % 2 == 0, np.nextafter(s, np.float32(0)),
+                     np.nextafter(s, np.float32(9)))
+        getattr(p, name)[page] = s.astype(np.float64)
+    x[:, 1:] = np.minimum(x[:, 1:], x[:, :1])
+    p.qkv = torch.from_numpy(np.tile(x.reshape(-1), 3)[None]).to(torch.bfloat16)
+    p.check_append()
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("scale", [1e-45, 9.2e-41, 1e-39, 1.3e-38, 3e38])
+def test_append_foreign_scales_at_the_ends_of_the_range(fmt, scale):
+    """Scales under 2^-126 (their reciprocal is no binary32 number) and next
+    to the largest number: with new tokens of zeros and of ordinary values."""
+    for zero in (True, False):
+        p = Problem(fmt, 2, 64, 32, [20, 40], [7, 1], q_heads=2, seed=4)
+        p.ks[:] = p.vs[:] = np.float64(np.float32(scale))
+        if zero:
+            p.qkv.zero_()
+        p.check_append()

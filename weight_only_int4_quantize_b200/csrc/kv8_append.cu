@@ -9,12 +9,16 @@
 //   new codes      round(x / s)                (ties to even; s = 0: 0)
 //   earlier codes  round(code * s0 / s)        only where s > s0
 //
-// With s of 8 significant bits every rounding is decided exactly: a code's
-// rounding border times s has at most 16 bits (and so has code * s0), x has
-// 8, so a quotient that is not on its border is at least 2^-17 (relative) away from
-// it.  x * (1 / s), off by less than 2^-22, rounded to 20 significant bits,
-// therefore falls on the same side, and back onto the border where it is on
-// it; no division is needed.
+// Every rounding is decided exactly.  With s (and s0) of 8 significant bits,
+// which is what this kernel writes, a code's rounding border times s has at
+// most 16 bits (and so has code * s0), x has 8, so a quotient that is not on
+// its border is at least 2^-17 (relative) away from it.  x * (1 / s), off by
+// less than 2^-22, rounded to 20 significant bits, therefore falls on the same
+// side, and back onto the border where it is on it; no division is needed.
+// A page's scale may also have come from elsewhere, with 24 bits: then both
+// sides have at most 32 bits, a quotient is at least 2^-33 away, and the same
+// is done in binary64 with 41 bits (write_exact).  That takes a page that held
+// earlier tokens, so one page of a sequence, head and side at most.
 //
 // A warp owns 16 tokens (a granule) of one page, kv head and side; the
 // page_size / 16 warps of a page share its largest magnitude through shared
@@ -79,6 +83,35 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float s0, float inv) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = snap(kv_value<FMT>(w >> (8 * i)) * s0 * inv);
   return kv_codes<FMT>(v[0], v[1], v[2], v[3]);
+}
+
+// A quotient off by less than 2^-51 as a float on the same side of every
+// border, or on it: to 41 significant bits, then rounded to odd.
+__device__ __forceinline__ float snap_exact(double v) {
+  const double w = __longlong_as_double((__double_as_longlong(v) + 0x800ll) & ~0xFFFll);
+  const float f = __double2float_rz(w);
+  return static_cast<double>(f) == w ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// Tokens first .. last - 1 of a granule at scales of any number of bits: a lane's
+// CH channels, `token` and `channel` bytes apart from `cell` on; tokens from
+// `fresh` on are new (rows `ld` apart from x on), those before are rescaled.
+template <int FMT, int CH>
+__device__ __noinline__ void write_exact(uint8_t* cell, int token, int channel, int first, int last,
+                                         int fresh, const __nv_bfloat16* x, int64_t ld, float s0,
+                                         float s1) {
+  const double inv = 1.0 / static_cast<double>(s1);
+#pragma unroll 1
+  for (int t = first; t < last; ++t) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      uint8_t* at = cell + t * token + i * channel;
+      const double v = t >= fresh
+                           ? static_cast<double>(__bfloat162float(x[t * ld + i]))
+                           : static_cast<double>(kv_value<FMT>(*at)) * static_cast<double>(s0);
+      *at = static_cast<uint8_t>(kv_codes<FMT>(snap_exact(v * inv), 0.f, 0.f, 0.f));
+    }
+  }
 }
 
 // Bytes of `after` where tokens first .. first + 3 are new or rescaled
@@ -184,6 +217,17 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
   const bool again = lo > 0 && s1 > s0;
   const int from = again ? 0 : lo;  // bytes of tokens [from, hi) are written
   if (t0 >= hi || t0 + kGranule <= from) return;
+
+  // More than 8 significant bits, or no binary32 reciprocal.
+  if (((__float_as_uint(s1) | (again ? __float_as_uint(s0) : 0u)) & 0xFFFFu) != 0 ||
+      (s1 > 0.f && s1 < __uint_as_float(0x00800000u))) {
+    const int first = from > t0 ? from - t0 : 0, last = hi - t0 < kGranule ? hi - t0 : kGranule;
+    uint8_t* cell = is_v ? c.v + ((slot * D + lane * CH) << c.log_page) + t0
+                         : c.k + ((slot << c.log_page) + t0) * D + lane * CH;
+    write_exact<FMT, CH>(cell, is_v ? 1 : D, is_v ? page_size : 1, first, last, lo - t0, x, ld, s0,
+                         s1);
+    return;
+  }
 
   auto value = [&](int t, int i) {  // channel i of the lane, in units of the scale
     const uint32_t u = raw[t][i / 2];
