@@ -1,7 +1,9 @@
 """GPU tests of the microscaled and 8-bit KV cache operators at the ends of
 what their contracts allow.
 
-Appending is bit-exact against the binary64 oracle.
+Appending is bit-exact against the binary64 oracle, attention within the bound
+that test_gpu_lowp.py derives (its allowance of 1e-30 replaced by half of
+bf16's smallest spacing, 2^-134).
 """
 import numpy as np
 import pytest
@@ -80,3 +82,42 @@ def test_append_foreign_scales_at_the_ends_of_the_range(fmt, scale):
         if zero:
             p.qkv.zero_()
         p.check_append()
+
+
+# ------------------------------------------------------------ attention limits ----
+
+def attention_error(p, scale=None):
+    """Largest error of the kernel in units of its bound, which allows 2^-134
+    beside the relative terms, and the reference."""
+    got = w4.kv8_attention(p.part(0, p.q_heads), p.cache(), *p.batch(), scale=scale)
+    torch.cuda.synchronize()
+    sc = float(np.float32(p.d ** -0.5 if scale is None else scale))
+    rows = int(p.starts[-1])
+    ref, weight, reach = L.kv_attention(p.host(0, p.q_heads), p.kc, p.vc, p.ks, p.vs, p.table, p.lens,
+                                        p.starts, p.page, p.fmt, sc)
+    delta = (p.d / 16 + 24) * 2.0 ** -23 * reach[:rows]
+    bound = (2.0 ** -8 * np.abs(ref[:rows]) + (2.0 ** -11 + 2.0 ** -18 + 2 * delta) * weight[:rows] +
+             max(p.lens) * 2.0 ** -34 * p.vs.max() * L.QMAX[p.fmt] + 2.0 ** -134)
+    err = np.abs(got.cpu().double().numpy()[:rows] - ref[:rows])
+    assert not np.any(np.isnan(err))
+    return float(np.max(err / bound)), ref[:rows]
+
+
+KERNELS = [  # heads, q_heads, d, lens, news: the rows kernel with 8 and 16 rows, the tcgen05 kernel
+    (2, 4, 128, [700, 33], [1, 1]), (2, 4, 64, [300, 90], [1, 9]), (24, 48, 64, [400], [300]),
+    (24, 48, 128, [400, 290], [200, 290])]
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,q_heads,d,lens,news", KERNELS)
+@pytest.mark.parametrize("exponent", [-120, 0, 100, 125])
+def test_attention_values_at_the_ends_of_the_range(fmt, heads, q_heads, d, lens, news, exponent):
+    """Values whose largest lie next to 2^126: the outputs are averages of
+    them, so as finite.  Values near 2^-113, and ordinary ones."""
+    p = Problem(fmt, heads, d, 32, lens, news, q_heads, seed=21)
+    r = np.random.RandomState(exponent & 15)
+    top = 2.0 ** (exponent if exponent < 100 else exponent - (6 if fmt == "int8" else 8))
+    p.vs = np.where(r.rand(*p.vs.shape) < 0.5, top, top / 2)
+    worst, ref = attention_error(p)
+    assert np.all(np.isfinite(ref)) and np.any(ref != 0)
+    assert worst <= 1

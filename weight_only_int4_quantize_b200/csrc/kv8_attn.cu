@@ -70,12 +70,12 @@ struct AttnShape {
   static constexpr int kSlotBytes = kTileTokens * D;
   static constexpr int kRing = W * kSlots * kSlotBytes;
   // Joined partial of the CTA (read by the cluster's peers), apart from the
-  // ring: rows of D floats, then maxima and sums.
+  // ring: rows of D floats, then maxima, sums and the unit of the outputs.
   static constexpr int part = kRing;
   static constexpr int ml = part + 8 * NT * D * 4;
-  static constexpr int bytes = ml + 2 * 16 * 4;
+  static constexpr int bytes = ml + (2 * 16 + 4) * 4;
   // The warps' partials take the ring's place.
-  static_assert(W * 8 * NT * ((D + 4) * 4 + 8) <= kRing, "partials fit the ring");
+  static_assert(W * (8 * NT * ((D + 4) * 4 + 8) + 4) <= kRing, "partials fit the ring");
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -440,6 +440,11 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
   constexpr int kLd = D + 4;  // floats between rows
   float* wo = reinterpret_cast<float*>(smem) + warp * (kRows * kLd);  // [row][channel]
   float* wm = reinterpret_cast<float*>(smem) + kWarps * kRows * kLd;  // [warp][row] maxima, sums
+  float* wv = wm + 2 * kWarps * kRows;  // [warp] units (v_ref)
+  // Outputs stay in units of the largest v_ref until they have been divided by
+  // the sum: before, they carry the probabilities' 2^14 and the number of keys,
+  // and in units of 1 they could pass binary32's range where the result does not.
+  if (lane == 0) wv[warp] = v_ref;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -452,14 +457,18 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
       }
 #pragma unroll
       for (int j = 0; j < kDTiles; ++j) {
-        wo[row * kLd + 16 * j + g] = o[nt][j][x] * v_ref;
-        wo[row * kLd + 16 * j + 8 + g] = o[nt][j][2 + x] * v_ref;
+        wo[row * kLd + 16 * j + g] = o[nt][j][x];
+        wo[row * kLd + 16 * j + 8 + g] = o[nt][j][2 + x];
       }
     }
   __syncthreads();
   float* part = reinterpret_cast<float*>(smem + SM::part);
   float* part_ml = reinterpret_cast<float*>(smem + SM::ml);
   const float* all_o = reinterpret_cast<const float*>(smem);
+  float unit = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) unit = fmaxf(unit, wv[w]);
+  const float per_unit = unit > 0.f ? __frcp_rn(unit) : 0.f;
   auto store = [&](int row, int d, float4 v) {
     const int r = r0 + row;
     __nv_bfloat16* dst = a.out +
@@ -479,8 +488,9 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(wm[w * kRows + row] - at);
+      float f = ex2(wm[w * kRows + row] - at);
       sum += f * wm[(kWarps + w) * kRows + row];
+      f *= wv[w] * per_unit;
       const float4 x = *reinterpret_cast<const float4*>(all_o + (w * kRows + row) * kLd + d);
       v.x += f * x.x;
       v.y += f * x.y;
@@ -489,12 +499,14 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
     }
     if (ks == 1) {
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      store(row, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+      store(row, d, make_float4(v.x * inv * unit, v.y * inv * unit, v.z * inv * unit,
+                                v.w * inv * unit));
     } else {
       *reinterpret_cast<float4*>(part + row * D + d) = v;
       if (d == 0) {
         part_ml[row] = mx;
         part_ml[16 + row] = sum;
+        part_ml[32] = unit;
       }
     }
   }
@@ -508,14 +520,20 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
   for (int e = rank * total / ks + threadIdx.x; e < e1; e += kAttnThreads) {
     const int row = e / (D / 4), d = (e % (D / 4)) * 4;
     float mx = -INFINITY;
-    for (int p = 0; p < ks; ++p) mx = fmaxf(mx, cluster.map_shared_rank(part_ml, p)[row]);
+    for (int p = 0; p < ks; ++p) {
+      const float* ml = cluster.map_shared_rank(part_ml, p);
+      mx = fmaxf(mx, ml[row]);
+      unit = fmaxf(unit, ml[32]);
+    }
+    const float per_unit = unit > 0.f ? __frcp_rn(unit) : 0.f;
     const float at = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p = 0; p < ks; ++p) {
       const float* ml = cluster.map_shared_rank(part_ml, p);
-      const float f = ex2(ml[row] - at);
+      float f = ex2(ml[row] - at);
       sum += f * ml[16 + row];
+      f *= ml[32] * per_unit;
       const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, p) + row * D + d);
       v.x += f * x.x;
       v.y += f * x.y;
@@ -523,7 +541,8 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
       v.w += f * x.w;
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    store(row, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    store(row, d, make_float4(v.x * inv * unit, v.y * inv * unit, v.z * inv * unit,
+                              v.w * inv * unit));
   }
   cluster.sync();  // peers keep their partials until every reader is done
 }
