@@ -121,3 +121,15 @@ def test_attention_values_at_the_ends_of_the_range(fmt, heads, q_heads, d, lens,
     worst, ref = attention_error(p)
     assert np.all(np.isfinite(ref)) and np.any(ref != 0)
     assert worst <= 1
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,q_heads,d,lens,news", KERNELS)
+def test_attention_values_of_the_smallest_scale_appended(fmt, heads, q_heads, d, lens, news):
+    """Pages whose value scale is 2^-126, the smallest that appending writes:
+    the outputs are ordinary bf16 numbers of 8 significant bits."""
+    p = Problem(fmt, heads, d, 32, lens, news, q_heads, seed=21)
+    p.vs[:] = 2.0 ** -126
+    worst, ref = attention_error(p)
+    assert np.any(np.abs(ref) > 2.0 ** -124)
+    assert worst <= 1
