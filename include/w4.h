@@ -732,7 +732,9 @@ w4_status w4_kv8_append(const w4_kv8_cache* cache, const void* k_bf16, int64_t l
  * tcgen05 kernel that works on 256 rows.
  *
  * q_bf16     device bf16 [rows, q_heads, head_dim], tokens ldq elements apart
- *            (a multiple of 8).
+ *            (a multiple of 8).  A token and head with an infinity or NaN gets
+ *            no meaningful output (NaN but for scores of -infinity alone);
+ *            others are not affected.
  * out_bf16   device bf16 [rows, q_heads, head_dim]; rows of no sequence are
  *            left as they were.
  * Other arguments as w4_kv8_append.  Results do not depend on timing: every

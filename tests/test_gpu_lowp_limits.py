@@ -133,3 +133,20 @@ def test_attention_values_of_the_smallest_scale_appended(fmt, heads, q_heads, d,
     worst, ref = attention_error(p)
     assert np.any(np.abs(ref) > 2.0 ** -124)
     assert worst <= 1
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("heads,q_heads,d,lens,news", KERNELS)
+def test_attention_of_a_query_that_is_not_finite(heads, q_heads, d, lens, news, bad):
+    """It gives NaN, not zeros, for its own token and head, and changes no
+    other output."""
+    p = Problem("int8", heads, d, 32, lens, news, q_heads, seed=23)
+    clean = w4.kv8_attention(p.part(0, q_heads), p.cache(), *p.batch())
+    q = p.part(0, q_heads).clone()
+    token, head = int(p.starts[1]) - 1, q_heads - 1
+    q[token, head, 5] = bad
+    got = w4.kv8_attention(q, p.cache(), *p.batch())
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(got[token, head]).all())
+    got[token, head] = clean[token, head]
+    assert torch.equal(got, clean)

@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float la, lb;
       unpack2(l2, la, lb);
       const float l = la + lb;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool none = l == 0.f;
+      const float inv = 1.f / l;
       __nv_bfloat16* dst = a.out + out_row * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -450,10 +451,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t y[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-          // A row that sees nothing (l = 0) gets zeros whatever O holds.  v_ref
-          // comes last: v_ref / l could underflow where the result does not.
-          const float y0 = inv > 0.f ? __uint_as_float(o[2 * x]) * inv * v_ref : 0.f;
-          const float y1 = inv > 0.f ? __uint_as_float(o[2 * x + 1]) * inv * v_ref : 0.f;
+          // A row that sees nothing (l = 0) gets zeros whatever O holds; a sum
+          // that is not a number stays one.  v_ref comes last: v_ref / l could
+          // underflow where the result does not.
+          const float y0 = none ? 0.f : __uint_as_float(o[2 * x]) * inv * v_ref;
+          const float y1 = none ? 0.f : __uint_as_float(o[2 * x + 1]) * inv * v_ref;
           const __nv_bfloat162 q = __floats2bfloat162_rn(y0, y1);
           y[x] = *reinterpret_cast<const uint32_t*>(&q);
         }
