@@ -150,3 +150,15 @@ def test_attention_of_a_query_that_is_not_finite(heads, q_heads, d, lens, news, 
     assert bool(torch.isnan(got[token, head]).all())
     got[token, head] = clean[token, head]
     assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,q_heads,d,lens,news", KERNELS)
+def test_attention_value_scales_under_the_smallest_normal(fmt, heads, q_heads, d, lens, news):
+    """Value scales that another quantizer left under 2^-126: 1 / scale is no
+    binary32 number, but the outputs are ordinary bf16 subnormals."""
+    p = Problem(fmt, heads, d, 32, lens, news, q_heads, seed=22)
+    p.vs[:] = float(np.float32(2.0 ** -131))
+    worst, ref = attention_error(p)
+    assert np.any(np.abs(ref) > 2.0 ** -130)
+    assert worst <= 1

@@ -290,7 +290,9 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
     m[nt][0] = m[nt][1] = -INFINITY;
     l[nt][0] = l[nt][1] = 0.f;
   }
-  float v_ref = 0.f;  // largest value scale so far: o is in its units
+  // Largest value scale so far, which o is in units of; not under 2^-126, so
+  // that its reciprocal is a number.
+  float v_ref = 0x1p-126f;
 
   for (int i = 0; i < my_tiles; ++i) {
     const int tok0 = (t_begin + warp + i * kWarps) * kTileTokens;
@@ -334,8 +336,8 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
     if (kSlots == 2) issue_k(i + 1, slot_k, page); else issue_v(i + 1, slot_k, page);
     // ---- online softmax ----
     const bool all_seen = tok0 + kTileTokens - 1 <= first_limit;
-    float v_new = fmaxf(v_ref, column_max(sv));
-    const float v_inv = v_new > 0.f ? __frcp_rn(v_new) : 0.f;
+    const float v_new = fmaxf(v_ref, column_max(sv));
+    const float v_inv = __frcp_rn(v_new);
     const float v_old = v_ref * v_inv, v_rel = sv * v_inv;
     v_ref = v_new;
     uint32_t pb[NT][4][2];
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
   float unit = 0.f;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) unit = fmaxf(unit, wv[w]);
-  const float per_unit = unit > 0.f ? __frcp_rn(unit) : 0.f;
+  const float per_unit = __frcp_rn(unit);
   auto store = [&](int row, int d, float4 v) {
     const int r = r0 + row;
     __nv_bfloat16* dst = a.out +
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
       mx = fmaxf(mx, ml[row]);
       unit = fmaxf(unit, ml[32]);
     }
-    const float per_unit = unit > 0.f ? __frcp_rn(unit) : 0.f;
+    const float per_unit = __frcp_rn(unit);
     const float at = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(q_full(rtile));
     }
     float m = -INFINITY;  // what O and l are relative to
-    float v_ref = 0.f;
+    float v_ref = 0x1p-126f;  // at least: its reciprocal is a number
     uint64_t l2 = pack2(0.f, 0.f);  // the sum, in two halves
     // Scales of the tile's four granules: lane g < 4 fetches those of granule
     // g one tile ahead.
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       const float off = kTcShift - (m == -INFINITY ? 0.f : m);
       const uint64_t off2 = pack2(off, off);
-      const float inv_v = v_ref > 0.f ? __frcp_rn(v_ref) : 0.f;
+      const float inv_v = __frcp_rn(v_ref);
       uint32_t p[32];
       auto weights = [&](auto masks) {
 #pragma unroll
