@@ -11,7 +11,8 @@ import torch
 
 import weight_only_int4_quantize_b200 as w4
 from oracle import lowp_oracle as L
-from tests.test_gpu_lowp import KV, Problem
+from tests.test_gpu_lowp import DEV, KV, Problem
+from weight_only_int4_quantize_b200 import synth
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -162,3 +163,53 @@ def test_attention_value_scales_under_the_smallest_normal(fmt, heads, q_heads, d
     worst, ref = attention_error(p)
     assert np.any(np.abs(ref) > 2.0 ** -130)
     assert worst <= 1
+
+
+# ------------------------------------------------------------ long predecessors ----
+
+@pytest.fixture(scope="module")
+def slow_kernel():
+    """A call whose kernel runs for longer than a wait's limit of one second
+    on 60 SMs and lets its dependents start at once: attention over a long
+    sequence whose pages are all the same one."""
+    heads, page, d = 60, 128, 64
+    cache = w4.kv8_cache(1, heads, page, d, device=DEV)
+    q = torch.randn(128, heads, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    starts = torch.tensor([0, 128], dtype=torch.int32, device=DEV)
+
+    def call(pages):
+        table = torch.zeros(1, pages, dtype=torch.int32, device=DEV)
+        lens = torch.tensor([pages * page], dtype=torch.int32, device=DEV)
+        out = torch.empty_like(q)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+
+        def run(dependents=lambda: None):
+            a.record()
+            w4.kv8_attention(q, cache, table, lens, starts, 128, out=out)
+            got = dependents()
+            b.record()
+            torch.cuda.synchronize()
+            return a.elapsed_time(b) / 1e3, got
+        return run
+
+    call(16384)()
+    seconds, _ = call(16384)()
+    return call(min(2 ** 23, int(16384 * 1.4 / seconds)))
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("flags", [0, w4.LINEAR_STATIC_WEIGHTS])
+def test_linear_waits_for_a_long_predecessor(slow_kernel, fmt, flags):
+    """The linear is resident while the kernel in front of it runs, and its
+    waits' limit does not count that time."""
+    calls = []
+    for m, n, k in ((5, 256, 2048), (300, 512, 1024)):
+        w = w4.fp4_quantize(synth.normal_weight(n, k, 0.02, seed=n).to(DEV), fmt)
+        x = w4.fp4_quantize(synth.normal_activations(m, k, seed=m).to(DEV), fmt)
+        calls.append((*x, *w, fmt, flags))
+    want = [w4.fp4_linear(*c) for c in calls]
+    seconds, got = slow_kernel(lambda: [w4.fp4_linear(*c) for c in calls])
+    assert seconds > 1.1
+    assert w4.device_error(clear=True) == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -256,6 +256,9 @@ __global__ void __launch_bounds__(kFp4Threads)
     bool issued = false;
     int st = 0;
     uint32_t ph = 0;
+    // The loads wait for the preceding kernel, however long it runs: the limit
+    // of the waits below starts after it.
+    pdl_wait();
     for (int kb = 0; kb < num_kb; ++kb) {
       if (!mbar_wait(full(st), ph, abort_flag, err, kKernelIdFp4)) break;
       tc_fence_after();
@@ -671,6 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       bool issued = false;
       int st = 0;
       uint32_t ph = 0, buf = 0;
+      pdl_wait();  // as above: no limit runs while the preceding kernel does
       for (int i = 0; i < my_tiles && !*abort_flag; ++i) {
         // Both CTAs have read the last tile's accumulators.
         if (i > 0 && !mbar_wait_cluster(acc_empty, (i - 1) & 1u, abort_flag, err)) break;
