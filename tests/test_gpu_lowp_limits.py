@@ -213,3 +213,21 @@ def test_linear_waits_for_a_long_predecessor(slow_kernel, fmt, flags):
     assert w4.device_error(clear=True) == 0
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("symmetric", [True, False])
+@pytest.mark.parametrize("flags", [w4.LINEAR_PDL, w4.LINEAR_PDL | w4.LINEAR_STATIC_WEIGHTS])
+def test_int4_linear_waits_for_a_long_predecessor(slow_kernel, symmetric, flags):
+    """The same for the int4 linear's programmatic dependent launches: prefill
+    (its K has more stages than its ring) and both decode kernels."""
+    w = w4.quantize_pack(synth.normal_weight(256, 2048, 0.02, seed=3).to(DEV), symmetric)
+    calls = []
+    for m, kind in ((64, w4.LINEAR_FORCE_GEMM), (4, w4.LINEAR_DECODE_STREAM),
+                    (4, w4.LINEAR_DECODE_TILED)):
+        calls.append((synth.normal_activations(m, 2048, seed=m).to(DEV), *w, flags | kind))
+    want = [w4.w4a16_linear(*c) for c in calls]
+    for c, y in zip(calls, want):
+        seconds, got = slow_kernel(lambda: w4.w4a16_linear(*c))
+        assert seconds > 1.1
+        assert w4.device_error(clear=True) == 0
+        assert torch.equal(got, y)

@@ -312,6 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_f16(BM, NB, EPI == kEpiStoreBf16);
       bool issued = false;
+      // The loads of x wait for the preceding kernel, however long it runs: the
+      // limit of the waits below starts after it.
+      pdl_wait();
       for (int kb = 0; kb < num_kb; ++kb) {
         const int s = kb % kStages;
         const uint32_t ph = (kb / kStages) & 1u;
@@ -399,6 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int it = 0; it < NB / 128; ++it)
             dc[it] = dq_const(__half2float(__ushort_as_half(static_cast<uint16_t>(csz[it] & 0xFFFFu))),
                               __half2float(__ushort_as_half(static_cast<uint16_t>(csz[it] >> 16))));
+          // Static weights: the stages are filled ahead of the preceding
+          // kernel's end; the first wait for a free one starts after it.
+          if (pdl_static != 0 && kb == kStages) pdl_wait();
           if (!mbar_wait(empty(s), ph ^ 1u, abort_flag, err, kKernelIdGemm)) {
             stop = true;
             break;
