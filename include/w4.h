@@ -644,7 +644,8 @@ w4_status w4_fp4_quantize(const void* x_bf16, int64_t R, int64_t K, int64_t ldx,
  *
  * xcodes, xscales, xrow  x [M, K] as w4_fp4_quantize writes it.
  * wcodes, wscales, wrow  w [N, K] likewise (xrow, wrow: NULL iff W4_FP4_MX).
- * y_bf16     device bf16 [M, N] out.
+ * y_bf16     device bf16 [M, N] out.  1 <= M <= 2^31 - 384,
+ *            1 <= N <= 2^31 - 257.
  * flags      0 or W4_LINEAR_STATIC_WEIGHTS.  The kernels of this section are
  *            always launched as programmatic dependent launches and let the
  *            next one be scheduled early; without the flag each touches memory

@@ -962,7 +962,8 @@ w4_status w4_fp4_linear(const uint8_t* xcodes, const uint8_t* xscales, const flo
   if (!valid_fp4_format(format)) return W4_ERR_UNSUPPORTED;
   if ((format == W4_FP4_NV) != (xrow != nullptr) || (format == W4_FP4_NV) != (wrow != nullptr))
     return W4_ERR_INVALID_ARG;
-  if (M < 1 || N < 1 || !valid_k(K) || M > 0x7FFFFFFF - 256 || N > 0x7FFFFFFF - 256)
+  // The last tile's row numbers (384 tokens, 256 channels) are 32-bit too.
+  if (M < 1 || N < 1 || !valid_k(K) || M > 0x7FFFFFFF - 383 || N > 0x7FFFFFFF - 256)
     return W4_ERR_SHAPE;
   if (!aligned16(xcodes) || !aligned16(xscales) || !aligned16(wcodes) || !aligned16(wscales) ||
       !aligned16(y_bf16) || (xrow && !aligned16(xrow)) || (wrow && !aligned16(wrow)))
@@ -992,8 +993,7 @@ static w4_status check_kv8(const w4_kv8_cache* c, const int32_t* page_table, int
   if (log_page < 4 || log_page > 7) return W4_ERR_UNSUPPORTED;
   if (c->num_pages < 1 || c->kv_heads < 1 || max_pages < 1 || batch < 1 || rows < 1 ||
       max_new < 1 || c->kv_heads > 65535 || rows > 0x7FFFFFFF ||
-      max_pages > 0x40000000 >> log_page || batch * c->kv_heads > 0x7FFFFFFF || max_new > rows ||
-      batch > 0x7FFFFFFF)
+      max_pages > 0x40000000 >> log_page || batch > 0x7FFFFFFF / c->kv_heads || max_new > rows)
     return W4_ERR_SHAPE;
   if (!starts && (rows != batch || max_new != 1)) return W4_ERR_SHAPE;
   if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) ||
