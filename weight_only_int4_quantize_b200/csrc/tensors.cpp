@@ -177,13 +177,14 @@ PyObject* fp4_quantize(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   NARGS(3, "fp4_quantize");
   int64_t block = 0;
   const int fmt = fp4_format(a[1], &block);
+  const int with_values = PyObject_IsTrue(a[2]);
+  if (with_values < 0) throw python_error();
   const Tensor& x = tensor(a[0], "x");
   check_dtype(x, ScalarType::BFloat16, "x");
   if (x.dim() != 2) throw value_error("x must be [R, K]");
   const int64_t r = x.size(0), k = x.size(1), ldx = row_stride(x, "x");
   check_cuda(x, "x");
   const c10::Device at = x.device();
-  const int with_values = PyObject_IsTrue(a[2]);
   const c10::cuda::CUDAGuard guard(at);
   const Tensor codes = empty({r, k / 2}, ScalarType::Byte, at);
   const Tensor scales = empty({(r + 127) / 128, k / (4 * block), 512}, ScalarType::Byte, at);
