@@ -1,6 +1,7 @@
 """Builds libw4.so in-tree with nvcc for sm_100a (no GPU needed to compile),
 and the _tensors extension (the tensor front end of the per-layer operators)
-with the C++ compiler against torch's headers.
+with the C++ compiler against torch's headers.  Without torch the library is
+built alone: the C ABI needs nothing else.
 
     python -m weight_only_int4_quantize_b200.build [--verbose]
 
@@ -63,7 +64,12 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-    build_tensors(verbose)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print("torch cannot be imported: the _tensors extension is not built", file=sys.stderr)
+    else:
+        build_tensors(verbose)
     return LIB
 
 
