@@ -40,3 +40,20 @@ def test_library_builds_where_torch_is_missing(tmp_path, monkeypatch, capsys):
     assert build.build() == str(tmp_path / "libw4.so")
     assert ran and not any("tensors.cpp" in a for cmd in ran for a in cmd)
     assert "_tensors" in capsys.readouterr().err
+
+
+def test_extension_that_cannot_be_loaded_says_why(lib, monkeypatch):  # noqa: F811
+    """Built, but against another torch: not reported as missing."""
+    class Broken:
+        def find_spec(self, name, path=None, target=None):
+            if name.endswith("._tensors"):
+                raise ImportError("undefined symbol: of_another_torch")
+
+    name = w4.__name__ + "._tensors"
+    monkeypatch.setattr(w4, "_TENSORS", None)
+    monkeypatch.delattr(w4, "_tensors", raising=False)
+    monkeypatch.delitem(sys.modules, name, raising=False)
+    monkeypatch.setattr(sys, "meta_path", [Broken(), *sys.meta_path])
+    with pytest.raises(RuntimeError, match="no fallback") as e:
+        w4.fp4_quantize(torch.zeros(1, 128, dtype=torch.bfloat16))
+    assert "of_another_torch" in str(e.value) and "missing" not in str(e.value)

@@ -11,6 +11,7 @@ any call fails loudly if the library has not been built
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import NamedTuple, Optional, Sequence
 
@@ -708,12 +709,13 @@ def _front_end():
     global _TENSORS
     if _TENSORS is None:
         L = lib()
+        how = "build it with `python -m weight_only_int4_quantize_b200.build` (no fallback exists)"
         try:
-            from . import _tensors as ext
-        except ImportError as e:
-            raise RuntimeError(
-                "the _tensors extension is missing: build it with "
-                "`python -m weight_only_int4_quantize_b200.build` (no fallback exists)") from e
+            ext = importlib.import_module(__name__ + "._tensors")
+        except ModuleNotFoundError as e:
+            raise RuntimeError(f"the _tensors extension is missing: {how}") from e
+        except ImportError as e:  # of another torch or Python, most often
+            raise RuntimeError(f"the _tensors extension cannot be loaded ({e}): {how}") from e
         ext.init(*[ctypes.cast(f, ctypes.c_void_p).value for f in
                    (L.w4_fp4_quantize, L.w4_fp4_linear, L.w4_kv8_append, L.w4_kv8_attention)],
                  W4Error)
