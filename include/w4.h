@@ -725,9 +725,15 @@ w4_status w4_kv8_append(const w4_kv8_cache* cache, const void* k_bf16, int64_t l
  * p = seq_lens[b] - n + i sees keys 0 .. p,
  *   out = softmax(scale * q . k) v,
  * query head h reading kv head h / (q_heads / kv_heads).  A token with p < 0
- * gets zeros.  Scores, sums and outputs in binary32; probabilities rounded to
- * fp16 (relative 2^-11; those under 2^-23 of the largest to a multiple of
- * 2^-33 of it), out once to bf16.  Single tokens and short runs take a kernel
+ * gets zeros.  Scores, sums and outputs in binary32, out once to bf16.  The
+ * products of probability and value scale are rounded to fp16 in units of the
+ * largest value scale that the sequence has for the head, which moves an
+ * output by at most
+ *   2^-11 sum_j p_j |v_j| + n 2^-34 V
+ * (n keys; V = qmax times that scale).  So a page whose value scale is far
+ * above the others' takes precision from them even where it has next to no
+ * weight: V should not be above some 2^20 times what the outputs amount to.
+ * Single tokens and short runs take a kernel
  * that works on 8 or 16 rows (tokens x heads of a group) at a time and splits
  * a sequence over a thread-block cluster of up to 16 CTAs; long runs take a
  * tcgen05 kernel that works on 256 rows.

@@ -165,6 +165,26 @@ def test_attention_value_scales_under_the_smallest_normal(fmt, heads, q_heads, d
     assert worst <= 1
 
 
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,q_heads,d,lens,news", KERNELS)
+@pytest.mark.parametrize("exponent", [10, 20, 30])
+def test_attention_beside_a_page_of_far_larger_value_scale(fmt, heads, q_heads, d, lens, news, exponent):
+    """A page that is hardly attended but whose value scale is 2^10 to 2^30
+    times the others': the outputs stay within the stated bound, whose term
+    n 2^-34 V is then the larger one."""
+    p = Problem(fmt, heads, d, 32, lens, news, q_heads, seed=24)
+    p.qkv[:, : q_heads * d] = p.qkv[:, : q_heads * d].abs() * 4
+    low = {"int8": 0x84, "e4m3": 0xFA}[fmt]  # -124, -320
+    for b in range(len(lens)):
+        p.kc[p.table[b, 0]] = low
+        p.ks[p.table[b, 0]] = p.ks.max()
+        p.vs[p.table[b, 0]] = p.vs.max()
+    for b in range(len(lens)):
+        p.vs[p.table[b, 0]] *= 2.0 ** exponent
+    worst, _ = attention_error(p)
+    assert worst <= 1
+
+
 # ------------------------------------------------------------ long predecessors ----
 
 @pytest.fixture(scope="module")
