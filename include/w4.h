@@ -754,9 +754,13 @@ w4_status w4_kv8_attention(const void* q_bf16, int64_t ldq, int64_t rows, int64_
 
 /*
  * w4_device_error -- reads (and with clear != 0 resets) the library's device
- * error word.  Every wait inside the tcgen05 kernels is bounded (about one
- * second); a kernel that gives up records it here and returns early, leaving
- * its outputs undefined but the CUDA context usable.  The KV cache kernels
+ * error word.  Every wait for a load or a tensor-core product is bounded
+ * (about one second, counted from the end of the preceding kernel); a kernel
+ * that gives up records it here and returns early, leaving its outputs
+ * undefined but the CUDA context usable.  Barriers among the threads of a CTA
+ * or cluster and the allocation of tensor memory have no limit: all threads
+ * reach the former also after a wait that gave up, and the latter waits for
+ * CTAs that free theirs without waiting for this kernel.  The KV cache kernels
  * record page ids, lengths and offsets that they skipped.  Synchronize the
  * streams that ran library kernels first.  Returns W4_OK,
  * W4_ERR_DEVICE_TIMEOUT (a wait gave up), W4_ERR_DEVICE_INDEX (only skipped

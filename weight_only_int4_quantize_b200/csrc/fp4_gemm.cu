@@ -21,7 +21,12 @@
 // epilogue.  K may be split over a thread-block cluster of up to 8 CTAs (few
 // tiles); the fp32 partial tiles are added through distributed shared memory
 // in rank order, so a launch configuration always gives the same bits.
-// Every wait is bounded; see w4_common.cuh.
+//
+// Every mbarrier wait is bounded; see w4_common.cuh.  Two kinds of waits are
+// not: CTA and cluster barriers, which every thread reaches, also after a wait
+// that gave up (no role returns early); and the allocation of tensor memory,
+// which waits for CTAs on the same SM to free theirs.  Those never wait for
+// this kernel: dependents are let start only once a CTA holds its own.
 #include <cooperative_groups.h>
 #include <cudaTypedefs.h>
 
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kFp4Threads)
     tma_prefetch_desc(&tx);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), T::kTmemCols);
+    tmem_alloc(smem_u32(tmem_slot), T::kTmemCols);  // no limit: see above
     tmem_relinquish();
   }
   tc_fence_before();
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(kFp4Threads)
 
   if (ks > 1) {
     // Every thread of every CTA of the cluster passes both barriers, also
-    // after a timeout, so none is left waiting.
+    // after a timeout, so none is left waiting (they have no limit of their own).
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();  // all partial tiles written
     if (warp >= 2 && !*abort_flag) {
@@ -606,7 +611,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   }
   tc_fence_before();
   cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();  // barriers of both CTAs are initialized
+  // Barriers of both CTAs are initialized.  Neither the allocation above nor the
+  // three cluster barriers have a limit: a cluster's CTAs start together, and
+  // all their threads reach each of them.
+  cluster.sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (threadIdx.x == 0) pdl_launch_dependents();  // holds its TMEM, as above

@@ -25,9 +25,10 @@
 // (0..7) uses channels 32t+4s..32t+4s+3, so the x operand of step s is two
 // consecutive bf16 pairs and needs no permutation.
 //
-// Every wait is bounded; a CTA that gives up records it in the device error
-// word, drains its own TMA loads and returns.  Every TMA load feeds only its
-// own CTA.
+// Every mbarrier wait is bounded; a CTA that gives up records it in the device
+// error word, drains its own TMA loads and returns (CTA and cluster barriers
+// have no limit: every thread reaches them, also then).  Every TMA load feeds
+// only its own CTA.
 #include <cooperative_groups.h>
 #include <cudaTypedefs.h>
 
