@@ -628,7 +628,8 @@ size_t w4_fp4_scale_bytes(int64_t R, int64_t K, int format);
  * row_scale_out  device float32 [R] out; NULL iff W4_FP4_MX.
  * values_bf16  device bf16 [R, K] out: the values that the codes stand for
  *            (exact in bf16 from 2^-126 up, rounded to its spacing of 2^-133
- *            below), or NULL.
+ *            below, infinite above its range: the largest of an nv row from
+ *            253 2^120 up stands for 264 2^120), or NULL.
  * Errors: W4_ERR_INVALID_ARG, W4_ERR_SHAPE, W4_ERR_ALIGNMENT (pointers 16
  * bytes), W4_ERR_UNSUPPORTED (format).
  */
@@ -640,7 +641,8 @@ w4_status w4_fp4_quantize(const void* x_bf16, int64_t R, int64_t K, int64_t ldx,
  * w4_fp4_linear -- y = x . w^T with both operands in microscaled 4-bit
  * floating point (same format), on the block-scaled tcgen05 tensor cores: the
  * products of codes are scaled by both blocks' scales and accumulated in
- * binary32; y = bf16(sum * xrow[m] * wrow[n]).  No bias.
+ * binary32; y = bf16(sum * wrow[n] * xrow[m]), each product rounded to
+ * binary32 and so within its range.  No bias.
  *
  * xcodes, xscales, xrow  x [M, K] as w4_fp4_quantize writes it.
  * wcodes, wscales, wrow  w [N, K] likewise (xrow, wrow: NULL iff W4_FP4_MX).
@@ -671,7 +673,9 @@ w4_status w4_fp4_linear(const uint8_t* xcodes, const uint8_t* xscales, const flo
  *            (W4_KV8_INT8, codes -127..127) or e4m3 (W4_KV8_E4M3).
  * v_codes    device [num_pages, kv_heads, head_dim, page_size] bytes (tokens
  *            contiguous).
- * k_scales, v_scales  device float32 [num_pages, kv_heads].
+ * k_scales, v_scales  device float32 [num_pages, kv_heads]: finite and not
+ *            negative, of any number of bits (another quantizer may have
+ *            filled the cache).
  * head_dim 64 or 128; page_size 16, 32, 64 or 128.
  *
  * A sequence's token p lies in page page_table[b][p / page_size].  Page ids,
@@ -712,7 +716,8 @@ typedef struct {
  *            starts[b] .. starts[b + 1] - 1 and take the last positions of
  *            its seq_lens[b]; or NULL: one new token each, row b.
  * max_new    at least the new tokens of any sequence (1 without starts).
- * Pages that take new tokens must belong to one sequence alone.
+ * Pages that take new tokens must belong to one sequence alone and appear
+ * once in its row of the table.
  */
 w4_status w4_kv8_append(const w4_kv8_cache* cache, const void* k_bf16, int64_t ldk,
                         const void* v_bf16, int64_t ldv, int64_t rows, const int32_t* page_table,
@@ -742,8 +747,16 @@ w4_status w4_kv8_append(const w4_kv8_cache* cache, const void* k_bf16, int64_t l
  *            (a multiple of 8).  A token and head with an infinity or NaN gets
  *            no meaningful output (NaN but for scores of -infinity alone);
  *            others are not affected.
+ * max_new    with `rows` and the heads, what the kernel is chosen by: a batch
+ *            of single tokens and one long run takes the kernel for long runs,
+ *            which does not split a sequence, for all.  Two calls, the single
+ *            tokens apart, are faster then (63 tokens and a run of 512 over
+ *            4096 keys each: 207 us, in one call 340).
  * out_bf16   device bf16 [rows, q_heads, head_dim]; rows of no sequence are
  *            left as they were.
+ * A cached key or value that is not finite may take the meaning of every new
+ * token of its sequence whose heads read it, also of those before it; other
+ * sequences and heads are not affected.
  * Other arguments as w4_kv8_append.  Results do not depend on timing: every
  * sum has a fixed order for a given call.
  */

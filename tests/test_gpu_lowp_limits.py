@@ -185,6 +185,24 @@ def test_attention_beside_a_page_of_far_larger_value_scale(fmt, heads, q_heads, 
     assert worst <= 1
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("side", ["ks", "vs"])
+@pytest.mark.parametrize("heads,q_heads,d,lens,news", KERNELS)
+def test_attention_keeps_a_spoilt_page_to_its_sequence_and_head(heads, q_heads, d, lens, news, side, bad):
+    """A page of one kv head whose scale is not finite, as appending an infinity
+    leaves it: the other heads' and sequences' outputs keep their bits."""
+    lens, news = (list(lens) + [150])[:2], (list(news) + [100])[:2]
+    p = Problem("e4m3", heads, d, 32, lens, news, q_heads, seed=25)
+    clean = w4.kv8_attention(p.part(0, q_heads), p.cache(), *p.batch())
+    getattr(p, side)[p.table[0, 1], heads - 1] = bad
+    got = w4.kv8_attention(p.part(0, q_heads), p.cache(), *p.batch())
+    group, rows = q_heads // heads, int(p.starts[1])
+    assert torch.equal(got[rows:], clean[rows:])
+    assert torch.equal(got[:rows, : q_heads - group], clean[:rows, : q_heads - group])
+    # the last token sees the page
+    assert bool(torch.isnan(got[rows - 1, q_heads - group:]).all())
+
+
 # ------------------------------------------------------------ long predecessors ----
 
 @pytest.fixture(scope="module")

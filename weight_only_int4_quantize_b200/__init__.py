@@ -729,14 +729,17 @@ def fp4_quantize(x, fmt: str = "mx", values: bool = False):
 
     Returns (codes uint8 [R, K/2], scale tiles uint8 [ceil(R/128), blocks/4,
     512], row scales float32 [R] or None for "mx"), and with values=True also
-    the bf16 [R, K] values that the codes stand for."""
+    the bf16 [R, K] values that the codes stand for.  Like the other operators
+    for serving, it is not differentiable: results carry no graph, also where x
+    requires a gradient."""
     return (_TENSORS or _front_end()).fp4_quantize(x, fmt, values)
 
 
 def fp4_linear(xcodes, xscales, xrow, wcodes, wscales, wrow, fmt: str = "mx", flags: int = 0,
                out=None):
     """y = x . w^T, bf16 [M, N], of an activation and a weight in the same
-    microscaled 4-bit format (each as fp4_quantize returns it)."""
+    microscaled 4-bit format (each as fp4_quantize returns it).  Not
+    differentiable."""
     return (_TENSORS or _front_end()).fp4_linear(xcodes, xscales, xrow, wcodes, wscales, wrow, fmt,
                                                flags, out)
 
@@ -744,7 +747,7 @@ def fp4_linear(xcodes, xscales, xrow, wcodes, wscales, wrow, fmt: str = "mx", fl
 class KV8Cache(NamedTuple):
     """An 8-bit paged KV cache: codes int8 or float8_e4m3fn, k_codes
     [pages, kv_heads, page_size, head_dim], v_codes [pages, kv_heads, head_dim,
-    page_size], and float32 scales [pages, kv_heads]."""
+    page_size], and float32 scales [pages, kv_heads], not negative."""
     k_codes: "torch.Tensor"
     v_codes: "torch.Tensor"
     k_scales: "torch.Tensor"
@@ -778,7 +781,8 @@ def kv8_append(cache, k, v, page_table, seq_lens, starts=None, max_new=None) -> 
     """Writes new keys and values (bf16 [rows, kv_heads, head_dim]; only the
     token axis may be strided) into the cache's pages.  seq_lens int32 [batch]
     counts the new tokens; starts int32 [batch + 1] gives each sequence's rows
-    (with max_new, at least the most of any), None one token each."""
+    (with max_new, at least the most of any), None one token each.  Writes the
+    cache's tensors in place; not differentiable."""
     (_TENSORS or _front_end()).kv8_append(cache, k, v, page_table, seq_lens, starts, max_new)
 
 
@@ -787,7 +791,7 @@ def kv8_attention(q, cache, page_table, seq_lens, starts=None, max_new=None, sca
     only the token axis may be strided) over the cache, which holds them
     already; other arguments as kv8_append.  scale: 1/sqrt(head_dim) if None.
     Returns bf16 [rows, q_heads, head_dim]; rows of no sequence are not
-    written."""
+    written.  Not differentiable."""
     return (_TENSORS or _front_end()).kv8_attention(q, cache, page_table, seq_lens, starts, max_new,
                                                   scale, out)
 

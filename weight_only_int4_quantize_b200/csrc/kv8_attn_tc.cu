@@ -685,8 +685,11 @@ cudaError_t launch_tc(const TcArgs& a, cudaStream_t stream, unsigned* err) {
 
 // Which kernel: per 64 keys the tcgen05 kernel takes 1.2 us (one row tile) or
 // 1.95 us (two) for each wave of CTAs, the rows kernel about 0.003 us for each
-// 16 rows of each problem (whatever the lengths, which the host does not
-// know, they enter both alike).  Measured, rows / tcgen05 kernel: 8 x 128
+// 16 rows of each problem.  The host knows neither the lengths, which enter
+// both alike, nor each sequence's new tokens: all are taken to have max_new,
+// so a batch of single tokens and one long run goes to the tcgen05 kernel,
+// which walks each single token's keys unsplit (one run of 512 and 63 single
+// tokens over 4096 keys each: 340 us, in two calls 207).  Measured, rows / tcgen05 kernel: 8 x 128
 // tokens over 4096 keys (16 / 8 heads) 156 / 100 us, 8 x 64 90 / 78, 8 x 16
 // 35 / 76; 1 x 256 over 16384 205 / 360; 2 x 2048 over 8192 917 / 254.
 bool kv8_attention_prefers_tc(const Kv8Cache& c, const Kv8Batch& bt, int group, int num_sms) {
