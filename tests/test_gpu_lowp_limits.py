@@ -203,6 +203,28 @@ def test_attention_keeps_a_spoilt_page_to_its_sequence_and_head(heads, q_heads, 
     assert bool(torch.isnan(got[rows - 1, q_heads - group:]).all())
 
 
+LONG_CONTEXTS = [  # heads, q_heads, d, page, lens, news
+    (1, 1, 64, 16, [3000], [1]), (8, 16, 128, 64, [9000], [1]), (8, 16, 64, 32, [32768], [1]),
+    (2, 8, 128, 128, [32768], [1]), (1, 4, 128, 128, [70000], [1]), (1, 1, 64, 64, [70001], [1]),
+    (2, 4, 128, 16, [9000, 70, 1], [1, 1, 1]), (4, 4, 64, 32, [64, 17, 20000, 0], [1, 1, 1, 0]),
+    (2, 8, 128, 64, [9000, 700], [9, 1]), (4, 16, 64, 64, [40, 12345], [9, 12]),
+    (16, 16, 128, 64, [5000, 31], [1, 1])]
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("heads,q_heads,d,page,lens,news", LONG_CONTEXTS)
+def test_attention_over_long_contexts(fmt, heads, q_heads, d, page, lens, news):
+    """Few problems and many key tiles: clusters of up to 16 CTAs (more than 8
+    are not portable sizes), CTAs of twelve warps, several tiles for each warp;
+    short and empty sequences beside a long one, whose clusters have CTAs
+    without a tile."""
+    p = Problem(fmt, heads, d, page, lens, news, q_heads, seed=sum(lens) + d, pad_rows=1)
+    p.check_attention()
+    p.ks = p.ks * 4
+    p.vs = p.vs * 2.0 ** np.random.RandomState(d).randint(-4, 5, p.vs.shape)
+    p.check_attention()
+
+
 # ------------------------------------------------------------ long predecessors ----
 
 @pytest.fixture(scope="module")
