@@ -434,7 +434,9 @@ __global__ void __launch_bounds__(kFp4Threads)
 // the loop and an elected lane issuing 0.62 us; with the loads signalling the
 // first CTA's barrier themselves, where a relaying thread of each CTA had
 // passed "stage full" on, 0.45 us (NB = 256: 0.30).  With every pair at work a
-// stage takes 0.57 (0.39) us: 8192 x 5120 x 17408 runs at 5.7 ... 5.9 PFLOP/s.
+// stage takes 0.57 (0.39) us: 8192 x 5120 x 17408 runs at 5.4 ... 5.9 PFLOP/s in
+// short bursts, and at 4.7 once the power limit has brought the SM clock down to
+// 1.2 GHz.
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 64 + 256;
 

@@ -25,11 +25,13 @@
 // memory.  A lane owns D / 32 neighbouring channels of all 16 tokens: rows are
 // read coalesced, key codes leave as words of a row, and the 16 codes of a
 // channel, which lie side by side in a value row, as one 16-byte store; nothing
-// is turned in shared memory.  Bound: for prompts instruction issue (4 of up
-// to 4000 tokens, 8 heads of 128: 17.4 us, where their 69 MB take 10.5; 21
-// without the path for granules that are new from end to end; a CTA per page
-// 52), for single tokens the chain of dependent loads (length, page id, rows
-// and scale).
+// is turned in shared memory.  Bound: for prompts the instructions of the
+// exact decisions at the occupancy that 64 registers leave (58 % of the issue
+// slots, 43 % of the warps; 4 of up to 4000 tokens, 8 heads of 128: 16.6 us,
+// where their 69 MB take 10.5; some 4 us more without the path for granules that
+// are new from end to end; a CTA per page 52), for single tokens the chain of
+// dependent loads (length, page id, rows and scale), in which write_exact adds
+// nothing that shows (64 tokens: 5.9 us either way).
 #include "kv8.cuh"
 #include "w4_kernels.h"
 

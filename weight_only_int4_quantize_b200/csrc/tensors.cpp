@@ -3,7 +3,7 @@
 // of the ctypes binding, the output allocations and the call into the C ABI
 // of libw4.so, as a CPython extension, because at a few microseconds of GPU
 // time per call the interpreter's share is what a user waits for (10 - 14 us
-// per call through ctypes, 4 - 5 us here).  No computation happens in it.
+// per call through ctypes, 3 - 5 us here).  No computation happens in it.
 //
 // The module is loaded by __init__.py, which hands it the addresses of the C
 // entry points (from the libw4.so it has loaded) and its W4Error class.
