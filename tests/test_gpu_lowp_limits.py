@@ -225,6 +225,47 @@ def test_attention_over_long_contexts(fmt, heads, q_heads, d, page, lens, news):
     p.check_attention()
 
 
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("batch,heads,q_heads,d,page", [(64, 8, 16, 128, 64), (32, 4, 4, 64, 16),
+                                                        (8, 8, 16, 64, 64)])
+def test_append_and_attention_without_a_pause(fmt, batch, heads, q_heads, d, page):
+    """Steps whose appends change the scale of every page, each kernel started
+    while the one before it runs: the same bits as with a wait between them."""
+    g = torch.Generator().manual_seed(batch)
+    table = torch.randperm(3 * batch, generator=g).int().view(batch, 3).to(DEV)
+    have, steps = page - 9, 6
+    first = torch.randn(batch * have, heads, d, generator=g).to(torch.bfloat16).to(DEV) * 0.01
+    new = [(torch.randn(batch, heads, d, generator=g) * 0.01 * 1.7 ** (i + 1)).to(torch.bfloat16).to(DEV)
+           for i in range(steps)]
+    q = torch.randn(batch, q_heads, d, generator=g).to(torch.bfloat16).to(DEV)
+    lens = [torch.full((batch,), have + i, dtype=torch.int32, device=DEV) for i in range(steps + 1)]
+    starts = torch.arange(0, batch * have + 1, have, dtype=torch.int32, device=DEV)
+    empty = w4.kv8_cache(3 * batch, heads, page, d, KV[fmt], DEV)
+    w4.kv8_append(empty, first, first, table, lens[0], starts, have)
+
+    def run(cache, pause):
+        for a, b in zip(cache, empty):
+            a.copy_(b)
+        out = []
+        for i in range(steps):
+            w4.kv8_append(cache, new[i], new[i], table, lens[i + 1])
+            pause()
+            out.append(w4.kv8_attention(q, cache, table, lens[i + 1]))
+            pause()
+        return out
+
+    calm, busy = (w4.KV8Cache(*[torch.empty_like(t) for t in empty]) for _ in range(2))
+    want = run(calm, torch.cuda.synchronize)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(busy, lambda: None)
+    for _ in range(20):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(busy, calm))
+
+
 # ------------------------------------------------------------ long predecessors ----
 
 @pytest.fixture(scope="module")
@@ -254,7 +295,7 @@ def slow_kernel():
 
     call(16384)()
     seconds, _ = call(16384)()
-    return call(min(2 ** 23, int(16384 * 1.4 / seconds)))
+    return call(min(2 ** 23, int(16384 * 1.6 / seconds)))
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
@@ -269,7 +310,7 @@ def test_linear_waits_for_a_long_predecessor(slow_kernel, fmt, flags):
         calls.append((*x, *w, fmt, flags))
     want = [w4.fp4_linear(*c) for c in calls]
     seconds, got = slow_kernel(lambda: [w4.fp4_linear(*c) for c in calls])
-    assert seconds > 1.1
+    assert seconds > 1.05
     assert w4.device_error(clear=True) == 0
     for a, b in zip(got, want):
         assert torch.equal(a, b)
@@ -288,6 +329,6 @@ def test_int4_linear_waits_for_a_long_predecessor(slow_kernel, symmetric, flags)
     want = [w4.w4a16_linear(*c) for c in calls]
     for c, y in zip(calls, want):
         seconds, got = slow_kernel(lambda: w4.w4a16_linear(*c))
-        assert seconds > 1.1
+        assert seconds > 1.05
         assert w4.device_error(clear=True) == 0
         assert torch.equal(got, y)

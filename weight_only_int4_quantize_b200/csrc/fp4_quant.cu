@@ -27,7 +27,8 @@
 // 17408: 69 us, 5.2 TB/s, with 384 threads of three pieces, two CTAs per SM, up
 // to 77 back to back; 83 with 544 of two and one CTA; 140 with 256 threads
 // whatever the row).  Rows of more than 18432 channels have two pieces and one
-// CTA per SM again, those of more than 32768 are read twice.  mx with values runs at 97 % of the copy rate (17408 x 5120: 63 us).
+// CTA per SM again, those of more than 32768 are read twice.  mx with values
+// runs at 97 % of the copy rate (17408 x 5120: 63 us).
 #include <type_traits>
 
 #include "fp4.cuh"

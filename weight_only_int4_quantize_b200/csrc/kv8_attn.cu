@@ -227,8 +227,10 @@ __global__ void __launch_bounds__(32 * W, AttnShape<D, NT, W>::kCtasPerSm)
   if (kSlots > 2) issue_k(1, 2, page_next);
   auto scales_of = [&](int p, float& sk, float& sv) {
     const int64_t at = static_cast<int64_t>(p < 0 ? 0 : p) * a.c.heads + h;
-    sk = p < 0 ? 0.f : __ldg(a.c.ks + at);
-    sv = p < 0 ? 0.f : __ldg(a.c.vs + at);
+    // Not through the non-coherent path: this kernel may be resident while an
+    // append writes these scales and reads their neighbours.
+    sk = p < 0 ? 0.f : a.c.ks[at];
+    sv = p < 0 ? 0.f : a.c.vs[at];
   };
   float sk_next, sv_next;
   scales_of(page, sk_next, sv_next);

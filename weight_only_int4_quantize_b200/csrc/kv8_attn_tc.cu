@@ -314,8 +314,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto scales_of = [&](int j) {
       const int p = (lane < 4 && j < my_tiles) ? page_of(j * kKeys + 16 * lane) : -1;
       const int64_t at = static_cast<int64_t>(p < 0 ? 0 : p) * a.c.heads + h;
-      sk_next = p < 0 ? 0.f : __ldg(a.c.ks + at);
-      sv_next = p < 0 ? 0.f : __ldg(a.c.vs + at);
+      // Not through the non-coherent path: this kernel may be resident while an
+      // append writes these scales and reads their neighbours.
+      sk_next = p < 0 ? 0.f : a.c.ks[at];
+      sv_next = p < 0 ? 0.f : a.c.vs[at];
     };
     scales_of(0);
     bool ok = true;
