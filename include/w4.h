@@ -747,7 +747,7 @@ w4_status w4_kv8_append(const w4_kv8_cache* cache, const void* k_bf16, int64_t l
  *            (a multiple of 8).  A token and head with an infinity or NaN gets
  *            no meaningful output (NaN but for scores of -infinity alone);
  *            others are not affected.
- * max_new    with `rows` and the heads, what the kernel is chosen by: a batch
+ * max_new    with the batch and the heads, what the kernel is chosen by: a batch
  *            of single tokens and one long run takes the kernel for long runs,
  *            which does not split a sequence, for all.  Two calls, the single
  *            tokens apart, are faster then (63 tokens and a run of 512 over

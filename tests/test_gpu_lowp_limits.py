@@ -266,6 +266,41 @@ def test_append_and_attention_without_a_pause(fmt, batch, heads, q_heads, d, pag
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(busy, calm))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_tensor_core_kernels_on_two_streams(d):
+    """The kernels that allocate tensor memory at the same time: prompt
+    attention on one stream, the 4-bit linear's two kernels and the int4
+    prefill on another, with the bits of calls that have the GPU to
+    themselves."""
+    p = Problem("int8", 24, d, 32, [600, 333], [600, 300], 48, seed=26)
+    cache, q, batch = p.cache(), p.part(0, 48), p.batch()
+    linears = []
+    for m, n, k, fmt in ((5, 2048, 2048, "mx"), (100, 1024, 2048, "nv"), (700, 2048, 1024, "nv")):
+        w = w4.fp4_quantize(synth.normal_weight(n, k, 0.02, seed=m).to(DEV), fmt)
+        linears.append((synth.normal_activations(m, k, seed=n).to(DEV), w, fmt))
+    packed = w4.quantize_pack(synth.normal_weight(2048, 1024, 0.02, seed=8).to(DEV), False)
+    x = synth.normal_activations(300, 1024, seed=9).to(DEV)
+
+    def attend():
+        return [w4.kv8_attention(q, cache, *batch)]
+
+    def multiply():
+        return [w4.fp4_linear(*w4.fp4_quantize(a, fmt), *w, fmt) for a, w, fmt in linears] + \
+            [w4.w4a16_linear(x, *packed, flags=w4.LINEAR_FORCE_GEMM | w4.LINEAR_PDL)]
+
+    work = [(torch.cuda.Stream(DEV), attend), (torch.cuda.Stream(DEV), multiply)]
+    want = [f() for _, f in work]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(15):
+        for (stream, f), g in zip(work, got):
+            with torch.cuda.stream(stream):
+                g.append(f())
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        assert all(torch.equal(a, b) for r in runs for a, b in zip(r, w))
+
+
 # ------------------------------------------------------------ long predecessors ----
 
 @pytest.fixture(scope="module")

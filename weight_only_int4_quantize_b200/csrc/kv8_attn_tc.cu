@@ -24,8 +24,8 @@
 // 2 x 2048 tokens over up to 8192 keys, 16 / 8 heads: 128 rows per CTA and
 // two CTAs per SM 371 us; 256 rows, one issuing warp, codes fetched into
 // registers one tile ahead 340 us; an issuing warp per row tile and copies
-// three tiles ahead 260 us; two S buffers with P in place 252 us, now
-// 249, 0.6 PFLOP/s (27 % of the tensor pipe).  What is left is the softmax arithmetic of eight
+// three tiles ahead 260 us; two S buffers with P in place 252 us, now 248, 0.6
+// PFLOP/s (27 % of the tensor pipe).  What is left is the softmax arithmetic of eight
 // warps, two per scheduler: 128-key tiles took 353 us, 128 us without that
 // arithmetic; 16 softmax warps of half a row each 381 us.
 //
@@ -691,7 +691,8 @@ cudaError_t launch_tc(const TcArgs& a, cudaStream_t stream, unsigned* err) {
 // both alike, nor each sequence's new tokens: all are taken to have max_new,
 // so a batch of single tokens and one long run goes to the tcgen05 kernel,
 // which walks each single token's keys unsplit (one run of 512 and 63 single
-// tokens over 4096 keys each: 340 us, in two calls 207).  Measured, rows / tcgen05 kernel: 8 x 128
+// tokens over 4096 keys each: 340 us, in two calls 207).
+// Measured, rows / tcgen05 kernel: 8 x 128
 // tokens over 4096 keys (16 / 8 heads) 156 / 100 us, 8 x 64 90 / 78, 8 x 16
 // 35 / 76; 1 x 256 over 16384 205 / 360; 2 x 2048 over 8192 917 / 249.
 bool kv8_attention_prefers_tc(const Kv8Cache& c, const Kv8Batch& bt, int group, int num_sms) {
